@@ -85,6 +85,7 @@ typedef enum { SV_DTYPE_F32 = 0, SV_DTYPE_BF16 = 1 } sv_dtype;
 #define SV_ROW_BAD_UNIFORM 16     /* T > 0 and some u_accept[b][j] or u_resample[b]
                                      outside [0, 1) or NaN */
 #define SV_ROW_BAD_TREE 32        /* spec_verify_tree: a parent index out of range */
+#define SV_ROW_BAD_SCORE 64       /* spec_verify_beam_select: a score that is NaN or +inf */
 
 /*
  * Bytes of device workspace spec_verify() needs for this shape (0 on a bad
@@ -454,6 +455,137 @@ sv_status spec_verify_lowrank_up(const void* u, const void* w_up, int M, int r, 
 sv_status spec_verify_lowrank_head(const void* h, const void* w_down, const void* w_up, int M, int d, int r,
                                    int V, const float* temperature, void* out_logits, double* out_lse,
                                    void* workspace, size_t workspace_bytes, int32_t* out_error,
+                                   struct CUstream_st* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The draft's full-rank head in 8-bit integers, in place of the low-rank one: the
+ * last hidden states are normed and quantised, a scale for each token, and
+ * multiplied with weights quantised once, a scale for each channel.  Products and
+ * sums are exact (int32), so the rounding of a logit comes from its two scales and
+ * its output type alone.  Infrastructure around [SlimSpec, Metodologia,
+ * "Arquitetura": the draft's LM head W_full h]; the pages give no 8-bit form.
+ *
+ * An int8 matrix [rows][K] has a row pitch ld (bytes): a multiple of 16, at least K
+ * ((K + 15) / 16 * 16 is the least).  The bytes of a row past K are neither read nor
+ * written.  K is at most SV_Q8_MAX_K, which keeps 128 * 128 * K below 2^31.
+ */
+#define SV_Q8_MAX_K 131056
+
+/*
+ * Rows to int8: out_scale[m] = max_k |x[m][k]| / 127 and out_q[m][k] =
+ * round(x[m][k] * 127 / max) (ties to even), what that formula gives in fp64.  A
+ * row of zeros has scale 0.  A row with NaN or inf has q = 0 and scale NaN, so its
+ * logits are NaN (SV_ROW_BAD_LOGITS in the verifier).
+ *   x [M][K] of dt, contiguous, 16-byte aligned;  out_q [M][ldq], 16-byte aligned
+ *   out_scale [M] float
+ * For weights: once, x = W [V][K].
+ */
+sv_status spec_verify_q8_quantize(const void* x, sv_dtype dt, int M, int K, int8_t* out_q, int ldq, float* out_scale,
+                                  struct CUstream_st* stream);
+
+/*
+ * Root-mean-square norm with the residual's addition, out in int8: with
+ * s = x + residual and p = s * weight (element by element),
+ *     rms = sqrt(mean_k s^2 + eps),  out_scale = max |p| / (127 rms),
+ *     out_q = round(p * 127 / max |p|)  (ties to even; what fp64 gives)
+ * so out_scale * out_q stands for p / rms.  The norm is of the unrounded sum.
+ *   x [M][d] of dt;  residual [M][d] of dt or null (0);  weight [d] of dt or null (1)
+ *   out_sum     optional [M][d] of dt: s rounded (the new residual stream); may be
+ *               exactly x or exactly residual
+ *   out_normed  optional [M][d] of dt: p / rms rounded (e.g. h of the low-rank head);
+ *               no other argument's memory
+ * Contiguous, 16-byte aligned (out_scale 4).  A row in which s or p is not finite in
+ * fp32: out_q = 0, out_scale and out_normed NaN.  eps: finite, >= 0 (0 with a row of
+ * zeros gives zeros).
+ */
+sv_status spec_verify_q8_norm(const void* x, const void* residual, const void* weight, sv_dtype dt, float eps, int M,
+                              int d, int8_t* out_q, int ldq, float* out_scale, void* out_sum, void* out_normed,
+                              struct CUstream_st* stream);
+
+/*
+ * out[m][v] = a_scale[m] * w_scale[v] * sum_k a[m][k] * w[v][k], rounded once to dt,
+ * on the tensor cores.
+ *   a [M][lda], w [V][ldw] int8;  a_scale [M], w_scale [V] float
+ *   out [M][V] of dt (the logits spec_verify, spec_verify_tree and
+ *   spec_verify_beam_select read), contiguous, 16-byte aligned
+ *   out_error  optional, device int32: as for spec_verify_lowrank_up
+ */
+sv_status spec_verify_q8_matmul(const int8_t* a, int lda, const float* a_scale, const int8_t* w, int ldw,
+                                const float* w_scale, int M, int K, int V, void* out, sv_dtype dt, int32_t* out_error,
+                                struct CUstream_st* stream);
+
+/* Workspace bytes of spec_verify_q8_head (the int8 rows and their scales); 0 on a bad
+ * shape.  It needs no initialisation. */
+size_t spec_verify_q8_head_workspace_size(int M, int d);
+
+/* spec_verify_q8_norm, then spec_verify_q8_matmul: from hidden states (of dt) to
+ * logits (of out_dt).  The workspace is 256-byte aligned; calls that share one must be
+ * ordered. */
+sv_status spec_verify_q8_head(const void* x, const void* residual, const void* weight, sv_dtype dt, float eps,
+                              const int8_t* w, int ldw, const float* w_scale, int M, int d, int V, void* out_sum,
+                              void* out_logits, sv_dtype out_dt, void* workspace, size_t workspace_bytes,
+                              int32_t* out_error, struct CUstream_st* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Growing a draft tree by beams [SpecLA, Metodologia 1: drafts shaped as branching
+ * trees; Metodologia 3: paths ranked by cumulative draft log-probability]: a level
+ * of K nodes is the K best continuations of the W nodes above it, and the draft's
+ * states follow the chosen parents.  The pages give no selection rule; this one is
+ * this library's reading.
+ */
+#define SV_MAX_BEAMS 32
+#define SV_BEAM_MAX_V (1 << 20)
+
+/* Workspace bytes of spec_verify_beam_select (256-byte aligned; needs no
+ * initialisation; calls that share one must be ordered); 0 on a bad shape. */
+size_t spec_verify_beam_workspace_size(int B, int W, int V, int K, sv_dtype dt);
+
+/*
+ * For every sequence b, the K best of the candidates (w, v), w < W, v < V:
+ *     key = score[b][w] + logits[b][w][v] / T - lse(logits[b][w] / T),  T = temperature[b]
+ * in decreasing key, ties to the lower beam, then the lower token (inside a beam the
+ * order is that of the logits).
+ * T = 0: a beam's one candidate is its first argmax, with key score[b][w].
+ * A frozen beam's one candidate is (pad_token, score[b][w]); its logits are not read.
+ * A beam of score -inf, and a token of logit -inf, give no candidate (a first level:
+ * score 0 for beam 0, -inf for the others).
+ *   logits       [B][W][V] of dt, contiguous, 16-byte aligned
+ *   score        [B][W] float;  temperature [B] float
+ *   frozen       optional [B][W] int32, nonzero = frozen; pad_token in [0, V) then
+ *   out_parent   [B][K] int32: w;  out_token [B][K] int32: v;  out_score [B][K]
+ *                float: the key (evaluated in fp64), the next level's score.  Slots
+ *                past the candidates hold -1, -1 and -inf.
+ *   out_row_status  optional [B] int32: SV_ROW_BAD_TEMPERATURE (nothing but frozen
+ *                beams is considered), SV_ROW_BAD_LOGITS (a row that is read holds NaN
+ *                or +inf, is all -inf, or its logits / T leave fp32's range from
+ *                above, or all of them from below), SV_ROW_BAD_SCORE (NaN or +inf); a
+ *                beam at fault gives no candidate.
+ * Limits: W and K in [1, SV_MAX_BEAMS], V in [1, SV_BEAM_MAX_V].  Two launches.
+ * spec_verify_tree's output law is the target's for children drawn independently
+ * from q; the best children are not that (greedy trees, verified with T = 0,
+ * excepted).  The key's fp32 sums decide between beams whose keys agree to ~1e-7.
+ */
+sv_status spec_verify_beam_select(const void* logits, sv_dtype dt, const float* score, const float* temperature,
+                                  const int32_t* frozen, int pad_token, int B, int W, int V, int K, int32_t* out_parent,
+                                  int32_t* out_token, float* out_score, int32_t* out_row_status, void* workspace,
+                                  size_t workspace_bytes, struct CUstream_st* stream);
+
+/*
+ * States follow the selected beams: for l < L, k < K, h < H and the first
+ * lengths[b] tokens (all S where lengths is null; a length is taken as within [0, S])
+ *     dst[l][b][k][h] = src[l][b][parent[b][k]][h]
+ * byte by byte.  Tokens past the length, and slots whose parent is outside [0, W)
+ * (e.g. -1), are left as they were.  dst and src must not overlap.
+ *   src [L][B][W][H][S][token_bytes], dst [L][B][K][H][S][token_bytes]: layers,
+ *   sequences, beams, heads, tokens; a state without tokens has H = S = 1.
+ *   16-byte accesses where both pointers and token_bytes are multiples of 16, 4, 2 or
+ *   1 otherwise.
+ *   parent [B][K] int32, lengths optional [B] int32: device memory
+ */
+sv_status spec_verify_beam_reorder(const void* src, void* dst, const int32_t* parent, const int32_t* lengths, int L,
+                                   int B, int W, int K, int H, long long S, long long token_bytes,
                                    struct CUstream_st* stream);
 
 #ifdef __cplusplus

@@ -25,12 +25,17 @@ EXPORTED = ("spec_verify", "spec_verify_workspace_size", "spec_verify_workspace_
             "spec_verify_bandit_state_size", "spec_verify_bandit_init", "spec_verify_bandit_step",
             "spec_verify_bandit_simulate", "spec_verify_tree", "spec_verify_tree_prune",
             "spec_verify_lowrank_workspace_size", "spec_verify_lowrank_down", "spec_verify_lowrank_up",
-            "spec_verify_lowrank_head")
+            "spec_verify_lowrank_head", "spec_verify_q8_quantize", "spec_verify_q8_norm", "spec_verify_q8_matmul",
+            "spec_verify_q8_head_workspace_size", "spec_verify_q8_head", "spec_verify_beam_workspace_size",
+            "spec_verify_beam_select", "spec_verify_beam_reorder")
 MAX_TOPF = 32
 MAX_ARMS = 16
 BANDIT_UCB1, BANDIT_THOMPSON, BANDIT_THOMPSON_BETA = 0, 1, 2
 MAX_TREE_NODES = 64
 ROW_BAD_TREE = 32
+ROW_BAD_SCORE = 64
+MAX_BEAMS = 32
+Q8_MAX_K = 131056
 
 _lib = None
 
@@ -88,6 +93,23 @@ def load_library(path: str = LIB_PATH):
     lib.spec_verify_lowrank_up.restype = i32
     lib.spec_verify_lowrank_head.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, sz, vp, vp]
     lib.spec_verify_lowrank_head.restype = i32
+    f32, i64 = ctypes.c_float, ctypes.c_longlong
+    lib.spec_verify_q8_quantize.argtypes = [vp, i32, i32, i32, vp, i32, vp, vp]
+    lib.spec_verify_q8_quantize.restype = i32
+    lib.spec_verify_q8_norm.argtypes = [vp, vp, vp, i32, f32, i32, i32, vp, i32, vp, vp, vp, vp]
+    lib.spec_verify_q8_norm.restype = i32
+    lib.spec_verify_q8_matmul.argtypes = [vp, i32, vp, vp, i32, vp, i32, i32, i32, vp, i32, vp, vp]
+    lib.spec_verify_q8_matmul.restype = i32
+    lib.spec_verify_q8_head_workspace_size.argtypes = [i32, i32]
+    lib.spec_verify_q8_head_workspace_size.restype = sz
+    lib.spec_verify_q8_head.argtypes = [vp, vp, vp, i32, f32, vp, i32, vp, i32, i32, i32, vp, vp, i32, vp, sz, vp, vp]
+    lib.spec_verify_q8_head.restype = i32
+    lib.spec_verify_beam_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+    lib.spec_verify_beam_workspace_size.restype = sz
+    lib.spec_verify_beam_select.argtypes = [vp, i32, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, sz, vp]
+    lib.spec_verify_beam_select.restype = i32
+    lib.spec_verify_beam_reorder.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, i64, i64, vp]
+    lib.spec_verify_beam_reorder.restype = i32
     if path == LIB_PATH:
         _lib = lib
     return lib
@@ -468,6 +490,243 @@ def lowrank_head(h: torch.Tensor, w_down: torch.Tensor, w_up: torch.Tensor, temp
                                                z.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
                                                error.data_ptr() if error is not None else None, s.cuda_stream))
     return z, lse
+
+
+# ---- the draft's step: 8-bit head, beams
+
+
+def _q8_stride(K: int) -> int:
+    return (K + 15) // 16 * 16
+
+
+def _cuda(t, name: str, dim: int) -> torch.device:
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda" or t.dim() != dim:
+        raise ValueError(f"{name} must be a {dim}-dimensional CUDA tensor")
+    return t.device
+
+
+def _check_q8(t: torch.Tensor, name: str, rows: int, K: int, device) -> int:
+    """An int8 [rows, K] matrix whose rows start at multiples of 16 bytes: its row pitch."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype != torch.int8:
+        raise TypeError(f"{name} must be torch.int8, got {t.dtype}")
+    if tuple(t.shape) != (rows, K):
+        raise ValueError(f"{name} must have shape {(rows, K)}, got {tuple(t.shape)}")
+    # the stride of a dimension of one element says nothing
+    ld = t.stride(0) if rows > 1 else _q8_stride(K)
+    if (K > 1 and t.stride(1) != 1) or ld < K or ld % 16:
+        raise ValueError(f"{name} must have rows of consecutive bytes at a pitch that is a multiple of 16 "
+                         "(as q8_quantize and q8_norm make them)")
+    return ld
+
+
+class _On:
+    """The device of the tensors and the stream of the call: what is allocated inside
+    belongs to that stream, so that its memory is not given away under a running kernel."""
+
+    __slots__ = ("device", "stream", "ctx")
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.ctx = device, stream, None
+
+    def __enter__(self):
+        if self.stream is not None:
+            self.ctx = torch.cuda.stream(self.stream)
+            self.ctx.__enter__()
+        elif torch.cuda.current_device() != self.device.index:
+            self.ctx = torch.cuda.device(self.device)
+            self.ctx.__enter__()
+        if self.stream is not None and self.stream.device != self.device:
+            self.__exit__(None, None, None)
+            raise ValueError(f"the stream must be on {self.device}, got {self.stream.device}")
+        return (self.stream if self.stream is not None else torch.cuda.current_stream(self.device)).cuda_stream
+
+    def __exit__(self, *a):
+        if self.ctx is not None:
+            self.ctx.__exit__(*a)
+            self.ctx = None
+
+
+def _q8_empty(rows: int, K: int, device):
+    q = torch.empty((rows, _q8_stride(K)), dtype=torch.int8, device=device)
+    return q[:, :K], torch.empty((rows,), dtype=torch.float32, device=device)
+
+
+def q8_quantize(x: torch.Tensor, *, stream: torch.cuda.Stream | None = None):
+    """Rows to int8 with a scale each: x [M, K] (float32 or bfloat16) -> (q [M, K] int8,
+    scale [M] float32).  q's rows start at multiples of 16 bytes, as ``q8_matmul`` takes
+    them; weights are quantised once with this."""
+    lib = load_library()
+    device = _cuda(x, "x", 2)
+    M, K = x.shape
+    dt = _dt_code(x.dtype)
+    _check(x, "x", None, (M, K), device)
+    with _On(device, stream) as s:
+        q, scale = _q8_empty(M, K, device)
+        _raise_if(lib.spec_verify_q8_quantize(x.data_ptr(), dt, M, K, q.data_ptr(), _q8_stride(K), scale.data_ptr(), s))
+    return q, scale
+
+
+def q8_norm(x: torch.Tensor, weight: torch.Tensor | None, eps: float, *, residual: torch.Tensor | None = None,
+            with_normed: bool = False, stream: torch.cuda.Stream | None = None):
+    """Root-mean-square norm with the residual's addition, out in int8 with a scale for
+    each row (see include/spec_verify.h): x, residual [M, d], weight [d] (None: ones), of
+    one type.  Returns (q [M, d] int8, scale [M] float32) plus, with ``residual``, the sum
+    x + residual [M, d], plus, with ``with_normed``, the normed rows [M, d], of x's type."""
+    lib = load_library()
+    device = _cuda(x, "x", 2)
+    M, d = x.shape
+    dt = _dt_code(x.dtype)
+    _check(x, "x", None, (M, d), device)
+    if weight is not None:
+        _check(weight, "weight", x.dtype, (d,), device)
+    if residual is not None:
+        _check(residual, "residual", x.dtype, (M, d), device)
+    with _On(device, stream) as s:
+        q, scale = _q8_empty(M, d, device)
+        total = torch.empty_like(x) if residual is not None else None
+        normed = torch.empty_like(x) if with_normed else None
+        _raise_if(lib.spec_verify_q8_norm(x.data_ptr(), residual.data_ptr() if residual is not None else None,
+                                          weight.data_ptr() if weight is not None else None, dt, eps, M, d,
+                                          q.data_ptr(), _q8_stride(d), scale.data_ptr(),
+                                          total.data_ptr() if total is not None else None,
+                                          normed.data_ptr() if normed is not None else None, s))
+    out = (q, scale)
+    if total is not None:
+        out += (total,)
+    if normed is not None:
+        out += (normed,)
+    return out
+
+
+def q8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+              dtype: torch.dtype = torch.bfloat16, *, error: torch.Tensor | None = None,
+              stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """a_scale[m] w_scale[v] sum_k a[m, k] w[v, k] on the tensor cores: a [M, K], w [V, K]
+    int8 (as ``q8_norm`` and ``q8_quantize`` make them), scales float32 -> [M, V] of
+    ``dtype`` (bfloat16 or float32), the logits that the verifier reads."""
+    lib = load_library()
+    device = _cuda(a, "a", 2)
+    M, K = a.shape
+    V = _cuda(w, "w", 2) and w.shape[0]
+    lda = _check_q8(a, "a", M, K, device)
+    ldw = _check_q8(w, "w", V, K, device)
+    _check(a_scale, "a_scale", torch.float32, (M,), device)
+    _check(w_scale, "w_scale", torch.float32, (V,), device)
+    if error is not None:
+        _check(error, "error", torch.int32, (1,), device)
+    dt = _dt_code(dtype)
+    with _On(device, stream) as s:
+        z = torch.empty((M, V), dtype=dtype, device=device)
+        _raise_if(lib.spec_verify_q8_matmul(a.data_ptr(), lda, a_scale.data_ptr(), w.data_ptr(), ldw, w_scale.data_ptr(),
+                                            M, K, V, z.data_ptr(), dt, error.data_ptr() if error is not None else None, s))
+    return z
+
+
+def q8_head(x: torch.Tensor, weight: torch.Tensor | None, eps: float, w: torch.Tensor, w_scale: torch.Tensor,
+            dtype: torch.dtype = torch.bfloat16, *, residual: torch.Tensor | None = None,
+            workspace: torch.Tensor | None = None, error: torch.Tensor | None = None,
+            stream: torch.cuda.Stream | None = None):
+    """``q8_norm`` then ``q8_matmul``: hidden states x [M, d] to logits [M, V] of ``dtype``;
+    with ``residual`` (logits, x + residual)."""
+    lib = load_library()
+    device = _cuda(x, "x", 2)
+    M, d = x.shape
+    xdt, dt = _dt_code(x.dtype), _dt_code(dtype)
+    V = _cuda(w, "w", 2) and w.shape[0]
+    _check(x, "x", None, (M, d), device)
+    ldw = _check_q8(w, "w", V, d, device)
+    _check(w_scale, "w_scale", torch.float32, (V,), device)
+    if weight is not None:
+        _check(weight, "weight", x.dtype, (d,), device)
+    if residual is not None:
+        _check(residual, "residual", x.dtype, (M, d), device)
+    if error is not None:
+        _check(error, "error", torch.int32, (1,), device)
+    if workspace is not None:
+        _check(workspace, "workspace", torch.uint8, (workspace.numel(),), device)
+    with _On(device, stream) as s:
+        if workspace is None:
+            workspace = torch.empty(lib.spec_verify_q8_head_workspace_size(M, d), dtype=torch.uint8, device=device)
+        z = torch.empty((M, V), dtype=dtype, device=device)
+        total = torch.empty_like(x) if residual is not None else None
+        _raise_if(lib.spec_verify_q8_head(x.data_ptr(), residual.data_ptr() if residual is not None else None,
+                                          weight.data_ptr() if weight is not None else None, xdt, eps, w.data_ptr(), ldw,
+                                          w_scale.data_ptr(), M, d, V, total.data_ptr() if total is not None else None,
+                                          z.data_ptr(), dt, workspace.data_ptr(), workspace.numel(),
+                                          error.data_ptr() if error is not None else None, s))
+    return z if total is None else (z, total)
+
+
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, temperature: torch.Tensor, K: int, *,
+                frozen: torch.Tensor | None = None, pad_token: int = 0, return_row_status: bool = False,
+                workspace: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None):
+    """The K best continuations of each sequence over its beams and the vocabulary by
+    cumulative log-probability (see include/spec_verify.h): logits [B, W, V] (float32 or
+    bfloat16), scores [B, W] and temperature [B] float32, frozen [B, W] int32 or None.
+    Returns (parent [B, K] int32, token [B, K] int32, score [B, K] float32) plus, if
+    asked, row_status [B] int32."""
+    lib = load_library()
+    device = _cuda(logits, "logits", 3)
+    B, W, V = logits.shape
+    K = int(K)
+    dt = _dt_code(logits.dtype)
+    _check(logits, "logits", None, (B, W, V), device)
+    _check(scores, "scores", torch.float32, (B, W), device)
+    _check(temperature, "temperature", torch.float32, (B,), device)
+    if frozen is not None:
+        _check(frozen, "frozen", torch.int32, (B, W), device)
+    if workspace is not None:
+        _check(workspace, "workspace", torch.uint8, (workspace.numel(),), device)
+    need = lib.spec_verify_beam_workspace_size(B, W, V, K, dt)
+    if need == 0:
+        raise SpecVerifyError(1, f"beam_select takes W and K in [1, {MAX_BEAMS}], V in [1, {1 << 20}] and B >= 1; got "
+                                 f"B={B}, W={W}, V={V}, K={K}")
+    with _On(device, stream) as s:
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        parent = torch.empty((B, K), dtype=torch.int32, device=device)
+        token = torch.empty((B, K), dtype=torch.int32, device=device)
+        score = torch.empty((B, K), dtype=torch.float32, device=device)
+        status = torch.empty((B,), dtype=torch.int32, device=device) if return_row_status else None
+        _raise_if(lib.spec_verify_beam_select(logits.data_ptr(), dt, scores.data_ptr(), temperature.data_ptr(),
+                                              frozen.data_ptr() if frozen is not None else None, int(pad_token), B, W, V,
+                                              K, parent.data_ptr(), token.data_ptr(), score.data_ptr(),
+                                              status.data_ptr() if status is not None else None, workspace.data_ptr(),
+                                              workspace.numel(), s))
+    out = (parent, token, score)
+    return out + (status,) if return_row_status else out
+
+
+def beam_reorder(src: torch.Tensor, parent: torch.Tensor, *, out: torch.Tensor | None = None,
+                 lengths: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """The draft's states of the selected beams: src [L, B, W, H, S, D] of any type (layers,
+    sequences, beams, heads, tokens, values), parent [B, K] int32 -> out [L, B, K, H, S, D],
+    out[:, b, k] = src[:, b, parent[b, k]] for the first lengths[b] tokens ([B] int32; None:
+    all).  What is not copied (tokens past the length, slots of a parent outside [0, W)) is
+    left as it was: zeros in an ``out`` that this call makes.  out must not overlap src."""
+    lib = load_library()
+    device = _cuda(src, "src", 6)
+    L, B, W, H, S, D = src.shape
+    if not isinstance(parent, torch.Tensor) or parent.dim() != 2:
+        raise ValueError("parent must be a [B, K] tensor")
+    K = parent.shape[1]
+    _check(src, "src", None, (L, B, W, H, S, D), device)
+    _check(parent, "parent", torch.int32, (B, K), device)
+    if lengths is not None:
+        _check(lengths, "lengths", torch.int32, (B,), device)
+    if out is not None:
+        _check(out, "out", src.dtype, (L, B, K, H, S, D), device)
+    with _On(device, stream) as s:
+        if out is None:
+            out = torch.zeros((L, B, K, H, S, D), dtype=src.dtype, device=device)
+        _raise_if(lib.spec_verify_beam_reorder(src.data_ptr(), out.data_ptr(), parent.data_ptr(),
+                                               lengths.data_ptr() if lengths is not None else None, L, B, W, K, H, S,
+                                               D * src.element_size(), s))
+    return out
 
 
 def lowrank_to_device(w, device="cuda"):

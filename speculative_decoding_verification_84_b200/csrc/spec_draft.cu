@@ -1,0 +1,358 @@
+// spec_draft.cu -- C ABI of the draft's step upstream of verification: the 8-bit
+// head (sv_q8.cuh), and the selection of a tree's next level with the reordering of
+// the draft's states (sv_beam.cuh).  The operations are specified in
+// include/spec_verify.h.
+#include "spec_verify.h"
+
+#include <cuda.h>  // CUtensorMap: driver calls go through entry points
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <atomic>
+#include <mutex>
+
+#include "sv_common.cuh"
+#include "sv_host.cuh"
+#include "sv_q8.cuh"
+#include "sv_beam.cuh"
+
+namespace {
+
+using namespace sv;
+
+inline bool dt_ok(sv_dtype dt) { return dt == SV_DTYPE_F32 || dt == SV_DTYPE_BF16; }
+
+// ----------------------------------------------------------------------------- rows to int8
+
+template <int ESZ, int VEC, int NV>
+void q8_rows_go(const Q8RowsArgs& g, int threads, cudaStream_t st)
+{
+    // rows of one warp: eight to a CTA
+    const dim3 block(threads, threads == 32 ? 8 : 1);
+    sv_q8_rows<ESZ, VEC, NV><<<(unsigned)cdiv(g.M, block.y), block, 0, st>>>(g);
+}
+
+// A row in registers, by as few threads as keep it to 4 vectors (16 elements where
+// the rows are not 16-byte multiples) a thread, at most 256 threads while 4 vectors
+// a thread allow it; one warp a row, without barriers, where that is enough.
+template <int ESZ>
+cudaError_t q8_rows_launch(const Q8RowsArgs& g, cudaStream_t st)
+{
+    const bool vec = ((long long)g.d * ESZ) % 16 == 0;
+    const long long pieces = vec ? (long long)g.d * ESZ / 16 : g.d;
+    const int nvs[3] = {1, vec ? 2 : 4, vec ? 4 : 16};
+    int nv = nvs[2];
+    if (pieces > 32 * nv) {
+        for (int i = 0; i < 3; ++i)
+            if (cdiv(pieces, nvs[i]) <= 256) { nv = nvs[i]; break; }
+    } else {
+        for (int i = 0; i < 3; ++i)
+            if (cdiv(pieces, nvs[i]) <= 32) { nv = nvs[i]; break; }
+    }
+    const long long threads = cdiv(cdiv(pieces, nv), 32) * 32;
+    if (threads > 1024) {
+        sv_q8_rows_long<ESZ><<<(unsigned)g.M, 1024, 0, st>>>(g);
+    } else if (vec) {
+        if (nv == 1) q8_rows_go<ESZ, 16 / ESZ, 1>(g, (int)threads, st);
+        else if (nv == 2) q8_rows_go<ESZ, 16 / ESZ, 2>(g, (int)threads, st);
+        else q8_rows_go<ESZ, 16 / ESZ, 4>(g, (int)threads, st);
+    } else {
+        if (nv == 1) q8_rows_go<ESZ, 1, 1>(g, (int)threads, st);
+        else if (nv == 4) q8_rows_go<ESZ, 1, 4>(g, (int)threads, st);
+        else q8_rows_go<ESZ, 1, 16>(g, (int)threads, st);
+    }
+    return cudaGetLastError();
+}
+
+sv_status q8_rows(const Q8RowsArgs& g, sv_dtype dt, cudaStream_t st)
+{
+    const cudaError_t e = dt == SV_DTYPE_BF16 ? q8_rows_launch<2>(g, st) : q8_rows_launch<4>(g, st);
+    return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+sv_status q8_rows_check(const void* x, sv_dtype dt, int M, int d, const void* q, int ldq, const void* scale)
+{
+    if (!x || !q || !scale || M < 1 || d < 1 || d > SV_Q8_MAX_K || ldq < d || ldq % 16) return SV_ERR_INVALID_ARG;
+    if (!dt_ok(dt)) return SV_ERR_UNSUPPORTED_DTYPE;
+    if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4)) return SV_ERR_MISALIGNED;
+    return SV_OK;
+}
+
+// ----------------------------------------------------------------------------- the product
+
+// Tensor map of a row-major int8 [rows][K] matrix of row pitch ld, in boxes of
+// kQ8BK bytes x box_rows, 128-byte swizzle; elements past K and rows read as zero.
+bool q8_map(CUtensorMap* m, const void* base, long long rows, long long K, long long ld, int box_rows)
+{
+    TensorMapEncodeFn enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld};
+    const cuuint32_t box[2] = {(cuuint32_t)kQ8BK, (cuuint32_t)box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int ESZ>
+cudaError_t q8_gemm_launch(const void* a, long long lda, const void* w, long long ldw, Q8GemmArgs g, cudaStream_t st)
+{
+    // as few token tiles as 256 tokens each allow, all of one size
+    g.m_tiles = (int)cdiv(g.M, kQ8MaxNT);
+    g.nt = (int)(cdiv(cdiv(g.M, g.m_tiles), 16) * 16);
+    g.m_tiles = (int)cdiv(g.M, g.nt);
+    g.v_tiles = (int)cdiv(g.V, kQ8BM);
+    g.tmem_cols = 32;
+    while (g.tmem_cols < 2 * g.nt) g.tmem_cols *= 2;
+    const int stage = kQ8WBytes + g.nt * kQ8BK;
+    g.stages = std::min(kQ8MaxStages, (kQ8SmemMax - 1024) / stage);
+    CUtensorMap tw, ta;
+    if (!q8_map(&tw, w, g.V, g.K, ldw, kQ8BM) || !q8_map(&ta, a, g.M, g.K, lda, g.nt)) return cudaErrorInvalidValue;
+    static std::atomic<bool> ready[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices || !ready[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(sv_q8_gemm<ESZ>, cudaFuncAttributeMaxDynamicSharedMemorySize, kQ8SmemMax);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < kMaxDevices) ready[dev].store(true, std::memory_order_release);
+    }
+    const long long tiles = (long long)g.m_tiles * g.v_tiles;
+    const long long grid = std::min<long long>(tiles, device_sm_count());
+    sv_q8_gemm<ESZ><<<(unsigned)grid, kQ8Threads, 1024 + g.stages * stage, st>>>(tw, ta, g);
+    return cudaGetLastError();
+}
+
+sv_status q8_gemm_check(const void* a, int lda, const void* a_scale, const void* w, int ldw, const void* w_scale, int M,
+                        int K, int V, const void* out, sv_dtype dt, const void* err)
+{
+    if (!a || !a_scale || !w || !w_scale || !out || M < 1 || K < 1 || K > SV_Q8_MAX_K || V < 1 || V > SV_MAX_V ||
+        lda < K || lda % 16 || ldw < K || ldw % 16)
+        return SV_ERR_INVALID_ARG;
+    if (!dt_ok(dt)) return SV_ERR_UNSUPPORTED_DTYPE;
+    if (!aligned(a, 16) || !aligned(w, 16) || !aligned(out, 16) || !aligned(a_scale, 4) || !aligned(w_scale, 4) ||
+        !aligned(err, 4))
+        return SV_ERR_MISALIGNED;
+    return SV_OK;
+}
+
+// ----------------------------------------------------------------------------- beams
+
+struct BeamPlan {
+    int nv, nseg, seg;
+    size_t off_list, total;
+};
+
+// Segments as large as 8 vectors a thread (fewer lists to merge), smaller while that
+// leaves fewer than two CTAs an SM, never so small that a row has over kBeamMaxSegs.
+bool beam_plan(int B, int W, int V, int K, sv_dtype dt, BeamPlan* p)
+{
+    if (B < 1 || W < 1 || W > SV_MAX_BEAMS || K < 1 || K > SV_MAX_BEAMS || V < 1 || V > SV_BEAM_MAX_V || !dt_ok(dt))
+        return false;
+    const int vec = dt == SV_DTYPE_BF16 ? 8 : 4;
+    const long long rows = (long long)B * W;
+    int nv = kBeamMaxNV;
+    while (nv > 1 && rows * cdiv(V, kBeamThreads * vec * nv) < 2 * kSmCount &&
+           cdiv(V, (long long)kBeamThreads * vec * (nv / 2)) <= kBeamMaxSegs)
+        nv /= 2;
+    const long long n = cdiv(V, (long long)kBeamThreads * vec * nv);
+    p->nv = nv;
+    p->seg = (int)(cdiv(cdiv(V, n), vec) * vec);
+    p->nseg = (int)cdiv(V, p->seg);
+    if (rows * p->nseg > 0x7fffffffLL) return false;
+    p->off_list = align256(sizeof(float4) * kBeamWarps * (size_t)rows * p->nseg);
+    p->total = p->off_list + align256(sizeof(uint2) * (size_t)K * rows * p->nseg);
+    return true;
+}
+
+template <int ESZ>
+cudaError_t beam_rows(const BeamArgs& g, int nv, cudaStream_t st)
+{
+    const unsigned grid = (unsigned)((long long)g.B * g.W * g.nseg);
+    switch (nv) {
+    case 1: sv_beam_rows<ESZ, 1><<<grid, kBeamThreads, 0, st>>>(g); break;
+    case 2: sv_beam_rows<ESZ, 2><<<grid, kBeamThreads, 0, st>>>(g); break;
+    case 4: sv_beam_rows<ESZ, 4><<<grid, kBeamThreads, 0, st>>>(g); break;
+    default: sv_beam_rows<ESZ, 8><<<grid, kBeamThreads, 0, st>>>(g); break;
+    }
+    return cudaGetLastError();
+}
+
+template <class VT>
+cudaError_t reorder(ReorderArgs g, cudaStream_t st)
+{
+    const long long vecs = g.S * g.tb / (long long)sizeof(VT);
+    g.tx = 8;
+    while (g.tx < kReorderThreads && (long long)g.tx * kReorderU < vecs) g.tx *= 2;
+    const long long tiles = cdiv(vecs, (long long)g.tx * kReorderU), groups = cdiv(g.chunks, kReorderThreads / g.tx);
+    if (tiles > 0x7fffffffLL || groups > 0x7fffffffLL || tiles * groups > 0x7fffffffLL) return cudaErrorInvalidValue;
+    sv_beam_reorder<VT><<<(unsigned)(tiles * groups), kReorderThreads, 0, st>>>(g);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// ============================================================================= C ABI
+
+extern "C" sv_status spec_verify_q8_quantize(const void* x, sv_dtype dt, int M, int K, int8_t* out_q, int ldq,
+                                             float* out_scale, struct CUstream_st* stream)
+{
+    const sv_status s = q8_rows_check(x, dt, M, K, out_q, ldq, out_scale);
+    if (s != SV_OK) return s;
+    Q8RowsArgs g = {x, nullptr, nullptr, out_q, out_scale, nullptr, nullptr, ldq, M, K, 0.f, 0};
+    return q8_rows(g, dt, (cudaStream_t)stream);
+}
+
+extern "C" sv_status spec_verify_q8_norm(const void* x, const void* residual, const void* weight, sv_dtype dt, float eps,
+                                         int M, int d, int8_t* out_q, int ldq, float* out_scale, void* out_sum,
+                                         void* out_normed, struct CUstream_st* stream)
+{
+    const sv_status s = q8_rows_check(x, dt, M, d, out_q, ldq, out_scale);
+    if (s != SV_OK) return s;
+    if (!(eps >= 0.f && eps <= FLT_MAX)) return SV_ERR_INVALID_ARG;
+    if (!aligned(residual, 16) || !aligned(weight, 16) || !aligned(out_sum, 16) || !aligned(out_normed, 16))
+        return SV_ERR_MISALIGNED;
+    Q8RowsArgs g = {x, residual, weight, out_q, out_scale, out_sum, out_normed, ldq, M, d, eps, 1};
+    return q8_rows(g, dt, (cudaStream_t)stream);
+}
+
+extern "C" sv_status spec_verify_q8_matmul(const int8_t* a, int lda, const float* a_scale, const int8_t* w, int ldw,
+                                           const float* w_scale, int M, int K, int V, void* out, sv_dtype dt,
+                                           int32_t* out_error, struct CUstream_st* stream)
+{
+    const sv_status s = q8_gemm_check(a, lda, a_scale, w, ldw, w_scale, M, K, V, out, dt, out_error);
+    if (s != SV_OK) return s;
+    Q8GemmArgs g = {};
+    g.out = out;
+    g.a_scale = a_scale;
+    g.w_scale = w_scale;
+    g.err = out_error;
+    g.M = M;
+    g.V = V;
+    g.K = K;
+    const cudaError_t e = dt == SV_DTYPE_BF16 ? q8_gemm_launch<2>(a, lda, w, ldw, g, (cudaStream_t)stream)
+                                              : q8_gemm_launch<4>(a, lda, w, ldw, g, (cudaStream_t)stream);
+    return e == cudaSuccess ? SV_OK : (e == cudaErrorInvalidValue ? SV_ERR_INVALID_ARG : SV_ERR_CUDA);
+}
+
+extern "C" size_t spec_verify_q8_head_workspace_size(int M, int d)
+{
+    if (M < 1 || d < 1 || d > SV_Q8_MAX_K) return 0;
+    return align256((size_t)M * (size_t)((d + 15) / 16 * 16)) + align256((size_t)M * sizeof(float));
+}
+
+extern "C" sv_status spec_verify_q8_head(const void* x, const void* residual, const void* weight, sv_dtype dt, float eps,
+                                         const int8_t* w, int ldw, const float* w_scale, int M, int d, int V, void* out_sum,
+                                         void* out_logits, sv_dtype out_dt, void* workspace, size_t workspace_bytes,
+                                         int32_t* out_error, struct CUstream_st* stream)
+{
+    if (!workspace) return SV_ERR_INVALID_ARG;
+    if (!aligned(workspace, 256)) return SV_ERR_MISALIGNED;
+    const size_t need = spec_verify_q8_head_workspace_size(M, d);
+    if (!need) return SV_ERR_INVALID_ARG;
+    if (workspace_bytes < need) return SV_ERR_WORKSPACE_TOO_SMALL;
+    const int ld = (d + 15) / 16 * 16;
+    int8_t* q = static_cast<int8_t*>(workspace);
+    float* scale = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + align256((size_t)M * ld));
+    // both halves' arguments, before anything is launched
+    sv_status s = q8_gemm_check(q, ld, scale, w, ldw, w_scale, M, d, V, out_logits, out_dt, out_error);
+    if (s != SV_OK) return s;
+    s = spec_verify_q8_norm(x, residual, weight, dt, eps, M, d, q, ld, scale, out_sum, nullptr, stream);
+    if (s != SV_OK) return s;
+    return spec_verify_q8_matmul(q, ld, scale, w, ldw, w_scale, M, d, V, out_logits, out_dt, out_error, stream);
+}
+
+extern "C" size_t spec_verify_beam_workspace_size(int B, int W, int V, int K, sv_dtype dt)
+{
+    BeamPlan p;
+    return beam_plan(B, W, V, K, dt, &p) ? p.total : 0;
+}
+
+extern "C" sv_status spec_verify_beam_select(const void* logits, sv_dtype dt, const float* score, const float* temperature,
+                                             const int32_t* frozen, int pad_token, int B, int W, int V, int K,
+                                             int32_t* out_parent, int32_t* out_token, float* out_score,
+                                             int32_t* out_row_status, void* workspace, size_t workspace_bytes,
+                                             struct CUstream_st* stream)
+{
+    if (!logits || !score || !temperature || !out_parent || !out_token || !out_score || !workspace)
+        return SV_ERR_INVALID_ARG;
+    if (!dt_ok(dt)) return SV_ERR_UNSUPPORTED_DTYPE;
+    BeamPlan p;
+    if (!beam_plan(B, W, V, K, dt, &p)) return SV_ERR_INVALID_ARG;
+    if (frozen && (pad_token < 0 || pad_token >= V)) return SV_ERR_INVALID_ARG;
+    if (!aligned(logits, 16) || !aligned(score, 4) || !aligned(temperature, 4) || !aligned(frozen, 4) ||
+        !aligned(out_parent, 4) || !aligned(out_token, 4) || !aligned(out_score, 4) || !aligned(out_row_status, 4) ||
+        !aligned(workspace, 256))
+        return SV_ERR_MISALIGNED;
+    if (workspace_bytes < p.total) return SV_ERR_WORKSPACE_TOO_SMALL;
+    BeamArgs g = {};
+    g.logits = logits;
+    g.score = score;
+    g.temperature = temperature;
+    g.frozen = frozen;
+    g.part = static_cast<float4*>(workspace);
+    g.list = reinterpret_cast<uint2*>(static_cast<unsigned char*>(workspace) + p.off_list);
+    g.out_parent = out_parent;
+    g.out_token = out_token;
+    g.out_score = out_score;
+    g.out_status = out_row_status;
+    g.B = B;
+    g.W = W;
+    g.V = V;
+    g.K = K;
+    g.nseg = p.nseg;
+    g.seg = p.seg;
+    g.pad_token = pad_token;
+    cudaStream_t st = (cudaStream_t)stream;
+    cudaError_t e = dt == SV_DTYPE_BF16 ? beam_rows<2>(g, p.nv, st) : beam_rows<4>(g, p.nv, st);
+    if (e != cudaSuccess) return SV_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)B);
+    cfg.blockDim = dim3((unsigned)(32 * W));
+    cfg.dynamicSmemBytes = (size_t)W * K * (sizeof(double) + sizeof(int)) + 2 * sizeof(int) * (size_t)W;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, sv_beam_merge, g) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+extern "C" sv_status spec_verify_beam_reorder(const void* src, void* dst, const int32_t* parent, const int32_t* lengths,
+                                              int L, int B, int W, int K, int H, long long S, long long token_bytes,
+                                              struct CUstream_st* stream)
+{
+    if (!src || !dst || !parent || L < 1 || B < 1 || W < 1 || W > SV_MAX_BEAMS || K < 1 || K > SV_MAX_BEAMS || H < 1 ||
+        S < 1 || token_bytes < 1)
+        return SV_ERR_INVALID_ARG;
+    long long chunks, block, in, out;
+    if (__builtin_mul_overflow((long long)L * B, (long long)H, &chunks) || __builtin_mul_overflow(S, token_bytes, &block) ||
+        __builtin_mul_overflow(chunks, block, &in) || __builtin_mul_overflow(in, (long long)K, &out) ||
+        __builtin_mul_overflow(in, (long long)W, &in))
+        return SV_ERR_INVALID_ARG;
+    if (!aligned(parent, 4) || !aligned(lengths, 4)) return SV_ERR_MISALIGNED;
+    const uintptr_t s0 = (uintptr_t)src, d0 = (uintptr_t)dst;
+    if (s0 < d0 + (uintptr_t)out && d0 < s0 + (uintptr_t)in) return SV_ERR_INVALID_ARG;  // not in place
+    ReorderArgs g = {};
+    g.src = static_cast<const unsigned char*>(src);
+    g.dst = static_cast<unsigned char*>(dst);
+    g.parent = parent;
+    g.lengths = lengths;
+    g.S = S;
+    g.tb = token_bytes;
+    g.chunks = chunks;
+    g.B = B;
+    g.W = W;
+    g.K = K;
+    g.H = H;
+    const uintptr_t bits = s0 | d0 | (uintptr_t)token_bytes;
+    cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e = bits % 16 == 0 ? reorder<uint4>(g, st)
+                          : bits % 4 == 0 ? reorder<uint32_t>(g, st)
+                          : bits % 2 == 0 ? reorder<unsigned short>(g, st)
+                                          : reorder<unsigned char>(g, st);
+    return e == cudaSuccess ? SV_OK : (e == cudaErrorInvalidValue ? SV_ERR_INVALID_ARG : SV_ERR_CUDA);
+}

@@ -27,6 +27,7 @@
 #include <cstring>
 
 #include "sv_common.cuh"
+#include "sv_host.cuh"
 #include "sv_generic.cuh"
 #include "sv_pass.cuh"
 #include "sv_small.cuh"
@@ -39,12 +40,10 @@ namespace {
 
 using namespace sv;
 
-constexpr int kSmCount = 148;             // B200; used only to size the split of V
 constexpr int kPass1ChunkBytes = 32768;   // generic: bytes of one row streamed by one CTA
 constexpr int kPass1MinChunk = 1024;      // generic: elements
 constexpr int kPass2Chunk = 8192;         // generic: elements per residual CTA
 constexpr int kPass2MinChunk = 512;
-constexpr int kMaxDevices = 64;
 // streaming path: the last rows streamed that are meant to stay in L2 for the
 // draw (the rest load with an evict-first hint); about 2/3 of the 126 MB L2
 constexpr long long kL2KeepBytes = 80LL << 20;
@@ -62,9 +61,6 @@ struct Plan {
     // same call reads it
     size_t off_c32a, off_c32b, off_seq, off_gath, off_part, off_rsum, total;
 };
-
-__host__ inline long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
-inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 bool force_generic()
 {
@@ -133,21 +129,6 @@ bool make_plan(int B, int gamma, int V, sv_dtype dt, Plan* p)
     off = align256(off + sizeof(double) * (size_t)nrsum);
     p->total = p->small ? 256 : off;  // the small path keeps everything in registers
     return true;
-}
-
-int device_sm_count()
-{
-    static std::mutex mu;
-    static int cache[kMaxDevices] = {};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return kSmCount;
-    std::lock_guard<std::mutex> lock(mu);
-    if (!cache[dev]) {
-        int n = 0;
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = kSmCount;
-        cache[dev] = n;
-    }
-    return cache[dev];
 }
 
 // Resident CTAs per SM of a 256-thread kernel on the current device (cached per
@@ -350,8 +331,6 @@ cudaError_t launch(const Plan& p, const void* tgt, const void* dft, const int32_
     sv_resample<ESZ><<<(unsigned)g2, kThreads, 0, st>>>(g);
     return cudaGetLastError();
 }
-
-inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 }  // namespace
 
@@ -792,25 +771,6 @@ extern "C" sv_status spec_verify_tree_prune(const void* draft_logits, sv_dtype d
 // ---------------------------------------------------------------------------- low-rank draft head
 
 namespace {
-
-typedef CUresult (*TensorMapEncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                      const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                      CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-TensorMapEncodeFn tensor_map_encoder()
-{
-    static TensorMapEncodeFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<TensorMapEncodeFn>(f);
-    });
-    return fn;
-}
 
 // Tensor map of a row-major [rows][K] bf16 matrix, in boxes of box_k (K) x
 // box_rows; out-of-range elements read as zero and are not written.
