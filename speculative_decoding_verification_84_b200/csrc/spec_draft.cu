@@ -23,51 +23,79 @@ using namespace sv;
 
 inline bool dt_ok(sv_dtype dt) { return dt == SV_DTYPE_F32 || dt == SV_DTYPE_BF16; }
 
+// Lets a kernel have `bytes` of dynamic shared memory, once per device.
+template <class Kernel>
+cudaError_t allow_smem(Kernel kernel, int bytes, std::atomic<bool> (&ready)[kMaxDevices])
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool known = dev >= 0 && dev < kMaxDevices;
+    if (known && ready[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && known) ready[dev].store(true, std::memory_order_release);
+    return e;
+}
+
 // ----------------------------------------------------------------------------- rows to int8
 
-template <int ESZ, int VEC, int NV>
-void q8_rows_go(const Q8RowsArgs& g, int threads, cudaStream_t st)
+constexpr int kQ8RowsSmemMax = 200 * 1024;  // three rows of x and of the residual
+
+template <int ESZ, int VEC, int NV, int MAXT>
+cudaError_t q8_rows_go(const Q8RowsArgs& g, int threads, cudaStream_t st)
 {
     // rows of one warp: eight to a CTA
     const dim3 block(threads, threads == 32 ? 8 : 1);
-    sv_q8_rows<ESZ, VEC, NV><<<(unsigned)cdiv(g.M, block.y), block, 0, st>>>(g);
+    const int all = threads * (int)block.y;
+    const size_t smem = VEC > 1 ? (size_t)kQ8RowSlots * (g.r ? 2 : 1) * NV * 16 * all : 0;
+    if (smem > 40 * 1024) {  // more than a kernel has without asking, static part included
+        static std::atomic<bool> ready[kMaxDevices];
+        const cudaError_t e = allow_smem(sv_q8_rows<ESZ, VEC, NV, MAXT>, kQ8RowsSmemMax, ready);
+        if (e != cudaSuccess) return e;
+    }
+    // as many CTAs as are resident at once, each walking rows
+    static std::atomic<int> regs;
+    int nreg = regs.load(std::memory_order_relaxed);
+    if (!nreg) {
+        cudaFuncAttributes a;
+        const cudaError_t e = cudaFuncGetAttributes(&a, sv_q8_rows<ESZ, VEC, NV, MAXT>);
+        if (e != cudaSuccess) return e;
+        nreg = (a.numRegs + 7) / 8 * 8;
+        regs.store(nreg, std::memory_order_relaxed);
+    }
+    const long long fit = std::min<long long>(std::min(2048 / all, 65536 / (nreg * all)), (long long)(226 * 1024 / (smem + 2048)));
+    const long long grid = std::min<long long>(cdiv(g.M, block.y), device_sm_count() * std::max<long long>(1, fit));
+    sv_q8_rows<ESZ, VEC, NV, MAXT><<<(unsigned)grid, block, smem, st>>>(g);
+    return cudaGetLastError();
 }
 
-// A row in registers, by as few threads as keep it to 4 vectors (16 elements where
-// the rows are not 16-byte multiples) a thread, at most 256 threads while 4 vectors
-// a thread allow it; one warp a row, without barriers, where that is enough.
-template <int ESZ>
+// A row by one warp, without barriers, where 4 pieces a thread (16 where the rows are
+// not 16-byte multiples and a piece is an element) are enough, else by up to 256 threads
+// with as few pieces each as that allows, else by up to 1024; beyond that from memory,
+// three times.
+template <int ESZ, int VEC>
 cudaError_t q8_rows_launch(const Q8RowsArgs& g, cudaStream_t st)
 {
-    const bool vec = ((long long)g.d * ESZ) % 16 == 0;
-    const long long pieces = vec ? (long long)g.d * ESZ / 16 : g.d;
-    const int nvs[3] = {1, vec ? 2 : 4, vec ? 4 : 16};
-    int nv = nvs[2];
-    if (pieces > 32 * nv) {
-        for (int i = 0; i < 3; ++i)
-            if (cdiv(pieces, nvs[i]) <= 256) { nv = nvs[i]; break; }
-    } else {
-        for (int i = 0; i < 3; ++i)
-            if (cdiv(pieces, nvs[i]) <= 32) { nv = nvs[i]; break; }
-    }
+    constexpr int N1 = VEC > 1 ? 1 : 4, N2 = VEC > 1 ? 2 : 8, N3 = VEC > 1 ? 4 : 16;
+    const long long pieces = cdiv(g.d, VEC);
+    const int room = pieces <= 32 * N3 ? 32 : 256;
+    const int nv = cdiv(pieces, N1) <= room ? N1 : (cdiv(pieces, N2) <= room ? N2 : N3);
     const long long threads = cdiv(cdiv(pieces, nv), 32) * 32;
-    if (threads > 1024) {
+    if (threads > 1024 || (VEC > 1 && (long long)kQ8RowSlots * (g.r ? 2 : 1) * nv * 16 * threads > kQ8RowsSmemMax)) {
         sv_q8_rows_long<ESZ><<<(unsigned)g.M, 1024, 0, st>>>(g);
-    } else if (vec) {
-        if (nv == 1) q8_rows_go<ESZ, 16 / ESZ, 1>(g, (int)threads, st);
-        else if (nv == 2) q8_rows_go<ESZ, 16 / ESZ, 2>(g, (int)threads, st);
-        else q8_rows_go<ESZ, 16 / ESZ, 4>(g, (int)threads, st);
-    } else {
-        if (nv == 1) q8_rows_go<ESZ, 1, 1>(g, (int)threads, st);
-        else if (nv == 4) q8_rows_go<ESZ, 1, 4>(g, (int)threads, st);
-        else q8_rows_go<ESZ, 1, 16>(g, (int)threads, st);
+        return cudaGetLastError();
     }
-    return cudaGetLastError();
+    if (threads > 256) return q8_rows_go<ESZ, VEC, N3, 1024>(g, (int)threads, st);
+    if (nv == N1) return q8_rows_go<ESZ, VEC, N1, 256>(g, (int)threads, st);
+    if (nv == N2) return q8_rows_go<ESZ, VEC, N2, 256>(g, (int)threads, st);
+    return q8_rows_go<ESZ, VEC, N3, 256>(g, (int)threads, st);
 }
 
 sv_status q8_rows(const Q8RowsArgs& g, sv_dtype dt, cudaStream_t st)
 {
-    const cudaError_t e = dt == SV_DTYPE_BF16 ? q8_rows_launch<2>(g, st) : q8_rows_launch<4>(g, st);
+    const bool bf = dt == SV_DTYPE_BF16, vec = (long long)g.d * (bf ? 2 : 4) % 16 == 0;
+    const cudaError_t e = bf ? (vec ? q8_rows_launch<2, 8>(g, st) : q8_rows_launch<2, 1>(g, st))
+                             : (vec ? q8_rows_launch<4, 4>(g, st) : q8_rows_launch<4, 1>(g, st));
     return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
@@ -111,14 +139,8 @@ cudaError_t q8_gemm_launch(const void* a, long long lda, const void* w, long lon
     CUtensorMap tw, ta;
     if (!q8_map(&tw, w, g.V, g.K, ldw, kQ8BM) || !q8_map(&ta, a, g.M, g.K, lda, g.nt)) return cudaErrorInvalidValue;
     static std::atomic<bool> ready[kMaxDevices];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    const cudaError_t e = allow_smem(sv_q8_gemm<ESZ>, kQ8SmemMax, ready);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= kMaxDevices || !ready[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(sv_q8_gemm<ESZ>, cudaFuncAttributeMaxDynamicSharedMemorySize, kQ8SmemMax);
-        if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < kMaxDevices) ready[dev].store(true, std::memory_order_release);
-    }
     const long long tiles = (long long)g.m_tiles * g.v_tiles;
     const long long grid = std::min<long long>(tiles, device_sm_count());
     sv_q8_gemm<ESZ><<<(unsigned)grid, kQ8Threads, 1024 + g.stages * stage, st>>>(tw, ta, g);
@@ -141,43 +163,52 @@ sv_status q8_gemm_check(const void* a, int lda, const void* a_scale, const void*
 // ----------------------------------------------------------------------------- beams
 
 struct BeamPlan {
-    int nv, nseg, seg;
-    size_t off_list, total;
+    int nb, Lsh;
+    size_t off_cmax, off_key, off_tok, off_info, off_ticket, total;
 };
 
-// Segments as large as 8 vectors a thread (fewer lists to merge), smaller while that
-// leaves fewer than two CTAs an SM, never so small that a row has over kBeamMaxSegs.
+// Batches of a row, and the lanes of a chunk: the most for which a row still has 2 K
+// chunks (the K best then hold little more than K logits at or above the least of
+// their maxima); a single lane's vector where no width gives that (V below 16 K).
 bool beam_plan(int B, int W, int V, int K, sv_dtype dt, BeamPlan* p)
 {
     if (B < 1 || W < 1 || W > SV_MAX_BEAMS || K < 1 || K > SV_MAX_BEAMS || V < 1 || V > SV_BEAM_MAX_V || !dt_ok(dt))
         return false;
     const int vec = dt == SV_DTYPE_BF16 ? 8 : 4;
+    p->nb = (int)cdiv(V, 32 * kBeamNV * vec);
+    p->Lsh = 5;
+    while (p->Lsh > 0 && cdiv(V, vec << p->Lsh) < 2 * K) --p->Lsh;
     const long long rows = (long long)B * W;
-    int nv = kBeamMaxNV;
-    while (nv > 1 && rows * cdiv(V, kBeamThreads * vec * nv) < 2 * kSmCount &&
-           cdiv(V, (long long)kBeamThreads * vec * (nv / 2)) <= kBeamMaxSegs)
-        nv /= 2;
-    const long long n = cdiv(V, (long long)kBeamThreads * vec * nv);
-    p->nv = nv;
-    p->seg = (int)(cdiv(cdiv(V, n), vec) * vec);
-    p->nseg = (int)cdiv(V, p->seg);
-    if (rows * p->nseg > 0x7fffffffLL) return false;
-    p->off_list = align256(sizeof(float4) * kBeamWarps * (size_t)rows * p->nseg);
-    p->total = p->off_list + align256(sizeof(uint2) * (size_t)K * rows * p->nseg);
+    if (rows > 0x7fffffffLL) return false;
+    p->off_cmax = align256(sizeof(float2) * (size_t)rows * p->nb);
+    p->off_key = p->off_cmax + align256(sizeof(float) * (size_t)rows * (size_t)(p->nb * kBeamNV << (5 - p->Lsh)));
+    p->off_tok = p->off_key + align256(sizeof(double) * (size_t)rows * K);
+    p->off_info = p->off_tok + align256(sizeof(int32_t) * (size_t)rows * K);
+    p->off_ticket = p->off_info + align256(sizeof(int2) * (size_t)rows);
+    p->total = p->off_ticket + align256(sizeof(unsigned) * (size_t)B);
     return true;
 }
 
-template <int ESZ>
-cudaError_t beam_rows(const BeamArgs& g, int nv, cudaStream_t st)
+template <int ESZ, bool AL>
+cudaError_t beam_go(const BeamArgs& g, cudaStream_t st)
 {
-    const unsigned grid = (unsigned)((long long)g.B * g.W * g.nseg);
-    switch (nv) {
-    case 1: sv_beam_rows<ESZ, 1><<<grid, kBeamThreads, 0, st>>>(g); break;
-    case 2: sv_beam_rows<ESZ, 2><<<grid, kBeamThreads, 0, st>>>(g); break;
-    case 4: sv_beam_rows<ESZ, 4><<<grid, kBeamThreads, 0, st>>>(g); break;
-    default: sv_beam_rows<ESZ, 8><<<grid, kBeamThreads, 0, st>>>(g); break;
-    }
-    return cudaGetLastError();
+    // one span of batches per resident warp
+    const long long batches = (long long)g.B * g.W * g.nb, warps = kBeamThreads / 32;
+    const long long per = cdiv(batches, (long long)device_sm_count() * 4 * warps);
+    if (per > 0x7fffffffLL) return cudaErrorInvalidValue;
+    sv_beam_rows<ESZ, AL><<<(unsigned)cdiv(cdiv(batches, per), warps), kBeamThreads, 0, st>>>(g, (int)per);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(g.B * g.W));
+    cfg.blockDim = dim3(kPickThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, sv_beam_pick<ESZ, AL>, g);
 }
 
 template <class VT>
@@ -292,8 +323,13 @@ extern "C" sv_status spec_verify_beam_select(const void* logits, sv_dtype dt, co
     g.score = score;
     g.temperature = temperature;
     g.frozen = frozen;
-    g.part = static_cast<float4*>(workspace);
-    g.list = reinterpret_cast<uint2*>(static_cast<unsigned char*>(workspace) + p.off_list);
+    g.part = static_cast<float2*>(workspace);
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    g.cmax = reinterpret_cast<float*>(ws + p.off_cmax);
+    g.key = reinterpret_cast<double*>(ws + p.off_key);
+    g.tok = reinterpret_cast<int32_t*>(ws + p.off_tok);
+    g.row_info = reinterpret_cast<int2*>(ws + p.off_info);
+    g.ticket = reinterpret_cast<unsigned*>(ws + p.off_ticket);
     g.out_parent = out_parent;
     g.out_token = out_token;
     g.out_score = out_score;
@@ -302,23 +338,14 @@ extern "C" sv_status spec_verify_beam_select(const void* logits, sv_dtype dt, co
     g.W = W;
     g.V = V;
     g.K = K;
-    g.nseg = p.nseg;
-    g.seg = p.seg;
+    g.nb = p.nb;
+    g.Lsh = p.Lsh;
     g.pad_token = pad_token;
     cudaStream_t st = (cudaStream_t)stream;
-    cudaError_t e = dt == SV_DTYPE_BF16 ? beam_rows<2>(g, p.nv, st) : beam_rows<4>(g, p.nv, st);
-    if (e != cudaSuccess) return SV_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)B);
-    cfg.blockDim = dim3((unsigned)(32 * W));
-    cfg.dynamicSmemBytes = (size_t)W * K * (sizeof(double) + sizeof(int)) + 2 * sizeof(int) * (size_t)W;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, sv_beam_merge, g) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+    const bool bf = dt == SV_DTYPE_BF16, al = (long long)V * (bf ? 2 : 4) % 16 == 0;  // every row on a 16-byte boundary
+    const cudaError_t e = bf ? (al ? beam_go<2, true>(g, st) : beam_go<2, false>(g, st))
+                             : (al ? beam_go<4, true>(g, st) : beam_go<4, false>(g, st));
+    return e == cudaSuccess ? SV_OK : (e == cudaErrorInvalidValue ? SV_ERR_INVALID_ARG : SV_ERR_CUDA);
 }
 
 extern "C" sv_status spec_verify_beam_reorder(const void* src, void* dst, const int32_t* parent, const int32_t* lengths,

@@ -6,21 +6,22 @@
 // The selection.  Candidate (w, v) of a sequence has the key
 //     score[w] + l[w][v] / T - lse(l[w] / T);
 // the K largest keys win, ties to the lower beam, then the lower token.  Inside a
-// beam the keys order as the logits do, whatever its normaliser, so ONE pass over
-// the logits gives both what the normaliser needs and the beam's best K logits:
-//   sv_beam_rows   one CTA per (row, segment): the segment in registers, each
-//                  warp's (offset, sum of exponentials), and the segment's best K
-//                  logits in order.  The K-th largest of the 32 maxima of groups
-//                  of 8 lanes bounds the K-th largest logit from below, so the
-//                  few elements at or above it (about K of them) are collected
-//                  and ranked by counting; if ties make them many, the K best are
-//                  taken one by one.
-//   sv_beam_merge  one CTA per sequence, a warp per beam: the row's normaliser in
-//                  fp64, its K best from the segments' sorted lists by K rounds of
-//                  a warp-wide maximum over the lists' heads; then one warp, a lane
-//                  per beam, takes the K best keys (fp64) the same way.  A
-//                  programmatic dependent of sv_beam_rows.
-// Segments are cut by token index, so equal rows give equal normalisers wherever
+// beam the keys order as the logits do, whatever its normaliser, and a row's K
+// best logits lie in the K chunks of largest maximum (ties: the earlier chunk, which
+// holds the smaller tokens).  So the pass over the logits selects nothing:
+//   sv_beam_rows   every warp walks a span of the rows: per batch of 4 vectors a
+//                  lane (offset, sum of exponentials), per chunk (L lanes of one
+//                  vector) its maximum.  No barrier, no shared memory.
+//   sv_beam_pick   one CTA per row: the normaliser in fp64; the K best chunks, of
+//                  which it reads the logits again (K L vectors, from L2); the
+//                  logits at or above the K-th chunk's maximum (about K), ranked
+//                  by counting.  The CTA that finishes a sequence's last row finds
+//                  every candidate's place among the beams' sorted keys (fp64) by
+//                  binary search.  A programmatic dependent of sv_beam_rows.
+// Selecting inside the pass (each CTA its segment's K best, with group maxima for
+// a threshold) cost more than the pass: 64 x 8 x 128256 bf16, K = 8, took 49 us in
+// that form against BEAM_ROWS_US.
+// Batches are cut by token index, so equal rows give equal normalisers wherever
 // they lie in memory.
 //
 // The states.  sv_beam_reorder copies dst[l][b][k] = src[l][b][parent[b][k]], the
@@ -32,53 +33,58 @@
 namespace sv {
 
 constexpr int kBeamThreads = 256;
-constexpr int kBeamWarps = kBeamThreads / 32;
-constexpr int kBeamMaxNV = 8;       // 16-byte vectors per thread
-constexpr int kBeamMaxSegs = 128;   // segments per row (4 lists per lane of the merge)
-constexpr int kBeamCap = 512;       // collected candidates of a segment
+constexpr int kBeamNV = 4;          // vectors a lane and batch
+constexpr int kPickThreads = 128;
+constexpr int kPickWarps = kPickThreads / 32;
+constexpr int kBeamCap = 512;       // candidates of a row
 
 struct BeamArgs {
     const void* logits;        // [B][W][V]
     const float* score;        // [B][W]
     const float* temperature;  // [B]
     const int32_t* frozen;     // [B][W] or null
-    float4* part;              // [B*W][nseg][kBeamWarps] (m, mk, s, 0)
-    uint2* list;               // [B*W][nseg][K] (logit bits, token), best first
+    float2* part;              // [B*W][nb] (max, sum) of each batch
+    float* cmax;               // [B*W][nch] chunk maxima, nch = nb * 4 * (32 / L)
+    double* key;               // [B*W][K] each row's candidates' keys, best first
+    int32_t* tok;              // [B*W][K] and tokens
+    int2* row_info;            // [B*W] (candidates, status bits)
+    unsigned* ticket;          // [B] rows finished
     int32_t* out_parent;       // [B][K]
     int32_t* out_token;        // [B][K]
     float* out_score;          // [B][K]
     int32_t* out_status;       // [B] or null
-    int B, W, V, K, nseg, seg;  // seg: tokens per segment, a multiple of the vector
+    int B, W, V, K, nb, Lsh;   // chunks of 2^Lsh lanes
     int pad_token;
 };
 
 __device__ __forceinline__ bool beam_t_ok(float T) { return T == 0.f || (T >= SV_TEMPERATURE_MIN && T <= FLT_MAX); }
 
-// A 16-byte vector of row elements [i, i + VEC) of a row that may start off a 16-byte
-// boundary; elements past V are -inf.  Reads only 16-byte blocks that hold a wanted
-// element, and no byte past `end`.
-template <int ESZ>
-__device__ __forceinline__ uint4 beam_ld(const unsigned char* row, int i, int V, const unsigned char* end)
+// Integer offset of a batch's sum: of its maximum, kept finite where a batch holds only
+// the type's lowest values (its sum is then 0).  T = 0 (khi = 1) needs the NaN test only.
+__device__ __forceinline__ float beam_offset(float m, float khi)
 {
-    constexpr int VEC = 16 / ESZ;
-    const unsigned char* p = row + (size_t)i * ESZ;
-    const unsigned sh = (unsigned)(reinterpret_cast<uintptr_t>(p) & 15u);
-    if (sh == 0 && i + VEC <= V) return ld_stream(reinterpret_cast<const uint4*>(p));
-    if (i + VEC <= V && p - sh + 32 <= end) {
-        const uint4* a = reinterpret_cast<const uint4*>(p - sh);
-        const uint4 lo = __ldg(a), hi = __ldg(a + 1);
-        const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-        const unsigned b = (sh & 3u) * 8u;
-        uint32_t o[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            // sh / 4 whole words, then sh % 4 bytes (sh is one value for the row)
-            const uint32_t a0 = sh < 4 ? w[k] : (sh < 8 ? w[k + 1] : (sh < 12 ? w[k + 2] : w[k + 3]));
-            const uint32_t a1 = sh < 4 ? w[k + 1] : (sh < 8 ? w[k + 2] : (sh < 12 ? w[k + 3] : w[(k + 4) & 7]));
-            o[k] = __funnelshift_r(a0, a1, b);
-        }
-        return make_uint4(o[0], o[1], o[2], o[3]);
-    }
+    return m == -INFINITY ? 0.f : fmaxf(ceilf(__fmul_rn(m, khi)), -3e38f);
+}
+
+__device__ __forceinline__ void beam_k(float T, float* khi, float* klo)
+{
+    *khi = 1.f;
+    *klo = 0x1p-60f;
+    if (T > 0.f) split_k(T, khi, klo);
+}
+
+// max over the warp (NaN ignored unless all are)
+__device__ __forceinline__ float beam_warp_max(float x)
+{
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+    return m;
+}
+
+// Row elements [i, i + VEC), element by element; -inf past V.
+template <int ESZ>
+__device__ __noinline__ uint4 beam_ld_edge(const unsigned char* p, int i, int V)
+{
     uint32_t o[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -93,8 +99,32 @@ __device__ __forceinline__ uint4 beam_ld(const unsigned char* row, int i, int V,
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// (value, index) ranks before: larger value, then smaller index
-__device__ __forceinline__ bool beam_before(float av, int ai, float bv, int bi) { return av > bv || (av == bv && ai < bi); }
+// 16 bytes starting `sh` bytes into the 32 of (lo, hi); sh is one value for the row.
+__device__ __forceinline__ uint4 beam_shift(const uint4& lo, const uint4& hi, unsigned sh)
+{
+    uint32_t w0 = lo.x, w1 = lo.y, w2 = lo.z, w3 = lo.w, w4 = hi.x, w5 = hi.y;
+    if (sh & 8u) { w0 = lo.z; w1 = lo.w; w2 = hi.x; w3 = hi.y; w4 = hi.z; w5 = hi.w; }
+    if (sh & 4u) { w0 = w1; w1 = w2; w2 = w3; w3 = w4; w4 = w5; }
+    const unsigned b = (sh & 3u) * 8u;
+    return make_uint4(__funnelshift_r(w0, w1, b), __funnelshift_r(w1, w2, b), __funnelshift_r(w2, w3, b),
+                      __funnelshift_r(w3, w4, b));
+}
+
+// Row elements [i, i + VEC), -inf past V, of a row that may start off a 16-byte
+// boundary: only blocks that hold an element of the row are read, and no byte past `end`.
+template <int ESZ, bool AL>
+__device__ __forceinline__ uint4 beam_ld(const unsigned char* row, int i, int V, const unsigned char* end)
+{
+    constexpr uint32_t ninf = ESZ == 2 ? 0xff80ff80u : 0xff800000u;
+    if (i >= V) return make_uint4(ninf, ninf, ninf, ninf);
+    const unsigned char* p = row + (size_t)i * ESZ;
+    if (AL) return ld_stream(reinterpret_cast<const uint4*>(p));
+    const unsigned sh = (unsigned)(reinterpret_cast<uintptr_t>(row) & 15u);
+    const unsigned char* a = p - sh;
+    if (i + 16 / ESZ <= V && a + 32 <= end)
+        return beam_shift(__ldg(reinterpret_cast<const uint4*>(a)), __ldg(reinterpret_cast<const uint4*>(a) + 1), sh);
+    return beam_ld_edge<ESZ>(p, i, V);
+}
 
 // Floats as integers of the same order (-0 first made +0).
 __device__ __forceinline__ unsigned beam_ord(float v)
@@ -103,145 +133,165 @@ __device__ __forceinline__ unsigned beam_ord(float v)
     return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
-template <int ESZ, int NV>
-__global__ void __launch_bounds__(kBeamThreads) sv_beam_rows(BeamArgs g)
+__device__ __forceinline__ float beam_unord(unsigned o)
 {
-    constexpr int VEC = 16 / ESZ;
-    __shared__ float s_group[32];
-    __shared__ float s_v[kBeamCap];
-    __shared__ int s_i[kBeamCap];
-    __shared__ float s_tau;
-    __shared__ int s_n;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int row = blockIdx.x / g.nseg, seg = blockIdx.x % g.nseg, b = row / g.W;
-    const float T = __ldg(g.temperature + b), sc = __ldg(g.score + row);
-    // no candidate comes from this row's logits
-    if (!beam_t_ok(T) || !(sc > -INFINITY && sc < INFINITY) || (g.frozen && __ldg(g.frozen + row))) return;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const unsigned char* base = static_cast<const unsigned char*>(g.logits);
-    const unsigned char* end = base + (size_t)g.B * g.W * g.V * ESZ;
-    const unsigned char* rp = base + (size_t)row * g.V * ESZ;
-    const int i0 = seg * g.seg, i1 = min(g.V, i0 + g.seg);
+    return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xffffffffu));
+}
 
+// (value, index) as one integer of the candidates' order: larger value, then smaller
+// index; 0 for -inf and NaN, which are no candidates.
+__device__ __forceinline__ unsigned long long beam_key(float v, int i)
+{
+    return v > -INFINITY ? (unsigned long long)beam_ord(v) << 32 | (0xffffffffu - (unsigned)i) : 0ull;
+}
+
+__device__ __forceinline__ unsigned long long beam_warp_max64(unsigned long long k)
+{
+    const unsigned hi = __reduce_max_sync(0xffffffffu, (unsigned)(k >> 32));
+    const unsigned lo = __reduce_max_sync(0xffffffffu, (unsigned)(k >> 32) == hi ? (unsigned)k : 0u);
+    return (unsigned long long)hi << 32 | lo;
+}
+
+// AL: every row starts on a 16-byte boundary (its length is then whole vectors).
+template <int ESZ, bool AL>
+__global__ void __launch_bounds__(kBeamThreads, 4) sv_beam_rows(BeamArgs g, int per_warp)
+{
+    constexpr int VEC = 16 / ESZ, NV = kBeamNV;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int lane = threadIdx.x & 31;
+    const int rows = g.B * g.W;
+    const long long first = ((long long)blockIdx.x * (kBeamThreads / 32) + (threadIdx.x >> 5)) * per_warp;
+    int left = (int)max(0ll, min((long long)per_warp, (long long)rows * g.nb - first));
+    int row = (int)(first / g.nb), batch = (int)(first % g.nb);
+    const unsigned char* base = static_cast<const unsigned char*>(g.logits);
+    const unsigned char* end = base + (size_t)rows * g.V * ESZ;
+    const int L = 1 << g.Lsh, cpv = 32 >> g.Lsh;  // lanes of a chunk, chunks of a warp's vector
+    for (int i = blockIdx.x * kBeamThreads + threadIdx.x; i < g.B; i += gridDim.x * kBeamThreads) g.ticket[i] = 0u;
+    if (left == 0) return;
+
+    // the row of batch `left`: whether any candidate comes from its logits
+    float T = 1.f;
+    auto look = [&](int r) {
+        T = __ldg(g.temperature + r / g.W);
+        const float sc = __ldg(g.score + r);
+        return beam_t_ok(T) && sc > -INFINITY && sc < INFINITY && !(g.frozen && __ldg(g.frozen + r));
+    };
+    auto load = [&](int r, int bt, uint4 (&v)[NV]) {
+        const unsigned char* rp = base + (size_t)r * g.V * ESZ;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) v[j] = beam_ld<ESZ, AL>(rp, ((bt * NV + j) * 32 + lane) * VEC, g.V, end);
+    };
+    float khi = 1.f, klo = 0.f;
     uint4 v[NV];
+    load(row, batch, v);  // before it is known whether the row counts: one batch at most is read in vain
+    bool live = look(row);
+    beam_k(T, &khi, &klo);
+    while (true) {
+        // the next batch of this row is on its way while this one is worked on
+        uint4 w[NV];
+        const bool more = left > 1 && batch + 1 < g.nb;
+        if (live && more) load(row, batch + 1, w);
+        if (live) {
+            float m[NV], mx;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int i = i0 + (j * kBeamThreads + tid) * VEC;
-        const uint32_t ninf = ESZ == 2 ? 0xff80ff80u : 0xff800000u;
-        v[j] = i < i1 ? beam_ld<ESZ>(rp, i, g.V, end) : make_uint4(ninf, ninf, ninf, ninf);
-    }
-    float m = vec_max<ESZ>(v[0]);
+            for (int j = 0; j < NV; ++j) m[j] = vec_max<ESZ>(v[j]);
+            if (L == 32) {
 #pragma unroll
-    for (int j = 1; j < NV; ++j) m = fmaxf(m, vec_max<ESZ>(v[j]));
-    const float tmax = m;
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if ((lane & 7) == 0) s_group[warp * 4 + (lane >> 3)] = m == m ? m : -INFINITY;
-    if (tid == 0) s_n = 0;
-#pragma unroll
-    for (int o = 8; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    // the warp's exponentials against its own integer offset (T = 0 needs the NaN test only)
-    {
-        float khi = 1.f, klo = 0x1p-60f;
-        if (T > 0.f) split_k(T, &khi, &klo);
-        // (kept finite where a warp holds only the type's lowest values: its sum is then 0)
-        const float mk = m == -INFINITY ? 0.f : fmaxf(ceilf(__fmul_rn(m, khi)), -3e38f);
-        unsigned long long acc[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] = pack2(0.f, 0.f);
-        lazy_exps_add<ESZ, NV>(acc, v, khi, klo, mk);
-        const float s = lazy_warp_sum(acc);
-        if (lane == 0) g.part[((size_t)row * g.nseg + seg) * kBeamWarps + warp] = make_float4(m, mk, s, 0.f);
-    }
-    __syncthreads();
-    if (warp == 0) {
-        // the K-th largest of the 32 group maxima
-        const float x = s_group[lane];
-        int rank = 0;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            const float y = __shfl_sync(0xffffffffu, x, j);
-            rank += (y > x || (y == x && j < lane)) ? 1 : 0;
-        }
-        if (rank == g.K - 1) s_tau = x;
-    }
-    __syncthreads();
-    const float tau = s_tau;
-    if (tmax >= tau) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            float x[VEC];
-            unpack<ESZ>(v[j], x);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                if (x[e] >= tau && x[e] > -INFINITY) {
-                    const int at = atomicAdd(&s_n, 1);
-                    if (at < kBeamCap) {
-                        s_v[at] = x[e];
-                        s_i[at] = i0 + (j * kBeamThreads + tid) * VEC + e;
-                    }
+                for (int j = 0; j < NV; ++j) m[j] = beam_warp_max(m[j]);
+                mx = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+                if (lane < NV) {
+                    const float x = lane == 0 ? m[0] : (lane == 1 ? m[1] : (lane == 2 ? m[2] : m[3]));
+                    g.cmax[((size_t)row * g.nb + batch) * NV + lane] = x;
                 }
-            }
-        }
-    }
-    __syncthreads();
-    const int n = s_n;
-    uint2* list = g.list + ((size_t)row * g.nseg + seg) * g.K;
-    if (n <= kBeamCap) {
-        for (int c = tid; c < n; c += kBeamThreads) {
-            const float x = s_v[c];
-            const int i = s_i[c];
-            int rank = 0;
-            for (int o = 0; o < n; ++o) rank += beam_before(s_v[o], s_i[o], x, i) ? 1 : 0;
-            if (rank < g.K) list[rank] = make_uint2(__float_as_uint(x), (unsigned)i);
-        }
-        for (int c = n + tid; c < g.K; c += kBeamThreads) list[c] = make_uint2(0xff800000u, 0xffffffffu);
-        return;
-    }
-    // many equal logits at the border: the best one after the last taken, K times
-    float lv = INFINITY;
-    int li = -1;
-    for (int k = 0; k < g.K; ++k) {
-        float bv = -INFINITY;
-        int bi = 0x7fffffff;
+            } else {
+                for (int o = 1; o < L; o <<= 1)
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            float x[VEC];
-            unpack<ESZ>(v[j], x);
+                    for (int j = 0; j < NV; ++j) m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], o));
+                if ((lane & (L - 1)) == 0)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const int i = i0 + (j * kBeamThreads + tid) * VEC + e;
-                if (beam_before(lv, li, x[e], i) && beam_before(x[e], i, bv, bi) && x[e] > -INFINITY) { bv = x[e]; bi = i; }
+                    for (int j = 0; j < NV; ++j)
+                        g.cmax[(((size_t)row * g.nb + batch) * NV + j) * cpv + (lane >> g.Lsh)] = m[j];
+                mx = beam_warp_max(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
             }
+            unsigned long long acc[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] = pack2(0.f, 0.f);
+            lazy_exps_add<ESZ, NV>(acc, v, khi, klo, beam_offset(mx, khi));
+            const float s = lazy_warp_sum(acc);
+            if (lane == 0) g.part[(size_t)row * g.nb + batch] = make_float2(mx, s);
         }
-        const unsigned o = beam_ord(bv), top = __reduce_max_sync(0xffffffffu, o);
-        const unsigned mi = __reduce_min_sync(0xffffffffu, o == top ? (unsigned)bi : 0x7fffffffu);
-        if (o == top && (unsigned)bi == mi) { s_v[warp] = bv; s_i[warp] = bi; }
-        __syncthreads();
-        bv = s_v[0];
-        bi = s_i[0];
-        for (int w = 1; w < kBeamWarps; ++w)
-            if (beam_before(s_v[w], s_i[w], bv, bi)) { bv = s_v[w]; bi = s_i[w]; }
-        __syncthreads();
-        lv = bv;
-        li = bi;
-        if (tid == 0) list[k] = make_uint2(__float_as_uint(bv), bv > -INFINITY ? (unsigned)bi : 0xffffffffu);
+        if (--left <= 0) return;
+        if (++batch == g.nb) {
+            batch = 0;
+            ++row;
+            const float before = T;
+            load(row, 0, v);
+            live = look(row);
+            if (T != before) beam_k(T, &khi, &klo);
+        } else {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) v[j] = w[j];
+        }
     }
 }
 
-// 32 W threads: warp w merges beam w.  Dynamic shared memory: W x K pairs.
-__global__ void __launch_bounds__(1024) sv_beam_merge(BeamArgs g)
+// The want best of n keys (larger first), one after the other, by the whole CTA:
+// each(f) calls f on every key of this thread; out(k, key) takes the k-th, 0 for none.
+template <class Each, class Out>
+__device__ __forceinline__ void pick_one_by_one(int want, unsigned long long* s_tmp, Each each, Out out)
 {
-    extern __shared__ __align__(8) unsigned char beam_dyn[];
-    double* s_key = reinterpret_cast<double*>(beam_dyn);         // [W][K]
-    int* s_tok = reinterpret_cast<int*>(s_key + g.W * g.K);      // [W][K]
-    int* s_cnt = s_tok + g.W * g.K;                              // [W]
-    int* s_bad = s_cnt + g.W;                                    // [W]
-    const int b = blockIdx.x, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const size_t row = (size_t)b * g.W + w;
+    unsigned long long last = ~0ull;
+    for (int k = 0; k < want; ++k) {
+        unsigned long long best = 0ull;
+        each([&](unsigned long long key) {
+            if (key < last && key > best) best = key;
+        });
+        best = beam_warp_max64(best);
+        if ((threadIdx.x & 31) == 0) s_tmp[threadIdx.x >> 5] = best;
+        __syncthreads();
+        best = s_tmp[0];
+        for (int i = 1; i < kPickWarps; ++i) best = max(best, s_tmp[i]);
+        __syncthreads();
+        last = best;
+        if (threadIdx.x == 0) out(k, best);
+    }
+}
+
+// How many of s_cand[0, n) rank before key; s_cand is 16-byte aligned and holds zeros
+// from n to the next multiple of 4.
+__device__ __forceinline__ int pick_rank(const unsigned long long* s_cand, int n, unsigned long long key)
+{
+    int rank = 0;
+#pragma unroll 2
+    for (int o = 0; o < n; o += 4) {
+        const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(s_cand + o);
+        const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(s_cand + o + 2);
+        rank += (a.x > key) + (a.y > key) + (c.x > key) + (c.y > key);
+    }
+    return rank;
+}
+
+template <int ESZ, bool AL>
+__global__ void __launch_bounds__(kPickThreads) sv_beam_pick(BeamArgs g)
+{
+    constexpr int VEC = 16 / ESZ, NU = 4, GROUPS = 64;
+    __shared__ float s_group[GROUPS];
+    __shared__ double s_sum[kPickWarps], s_lse;
+    __shared__ float s_top[kPickWarps];
+    __shared__ __align__(16) unsigned long long s_cand[kBeamCap + 4];
+    __shared__ unsigned long long s_tmp[kPickWarps];
+    __shared__ int s_sel[SV_MAX_BEAMS];
+    __shared__ float s_tau, s_low;
+    __shared__ int s_n, s_m, s_last;
+    const int row = blockIdx.x, b = row / g.W, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int nch = g.nb * kBeamNV << (5 - g.Lsh), CH = VEC << g.Lsh, L = 1 << g.Lsh;
     const float T = __ldg(g.temperature + b), sc = __ldg(g.score + row);
-    const bool frozen = g.frozen && __ldg(g.frozen + row);
-    const bool t_ok = beam_t_ok(T);
+    const bool frozen = g.frozen && __ldg(g.frozen + row), t_ok = beam_t_ok(T);
+    float khi, klo;
+    beam_k(t_ok ? T : 0.f, &khi, &klo);
+    double* key = g.key + (size_t)row * g.K;
+    int32_t* tok = g.tok + (size_t)row * g.K;
+    if (tid == 0) { s_n = 0; s_m = 0; s_low = -INFINITY; }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     int cnt = 0, bad = 0;
     if (!(sc < INFINITY)) {
@@ -249,114 +299,216 @@ __global__ void __launch_bounds__(1024) sv_beam_merge(BeamArgs g)
     } else if (sc == -INFINITY) {
     } else if (frozen) {
         cnt = 1;
-        if (lane == 0) { s_key[w * g.K] = (double)sc; s_tok[w * g.K] = g.pad_token; }
+        if (tid == 0) { key[0] = (double)sc; tok[0] = g.pad_token; }
     } else if (t_ok) {
-        // the row's normaliser
-        float M_ = -INFINITY, MK = 0.f;
-        double S = 0.0;
-        int nan = 0;
-        const float4* part = g.part + row * g.nseg * kBeamWarps;
-        for (int t = lane; t < g.nseg * kBeamWarps; t += 32) {
-            const float4 p = part[t];
-            nan |= (p.z != p.z);
-            if (p.x == -INFINITY) continue;
-            if (M_ == -INFINITY) { M_ = p.x; MK = p.y; S = (double)p.z; continue; }
-            if (p.y > MK) { S = S * pow2d(MK - p.y) + (double)p.z; MK = p.y; }
-            else S += (double)p.z * pow2d(p.y - MK);
-            M_ = fmaxf(M_, p.x);
-        }
+        // ---- the chunks' maxima and the row's normaliser: batch sums against the largest
+        // offset, in fp64
+        const float* cmax = g.cmax + (size_t)row * nch;
+        const float2* part = g.part + (size_t)row * g.nb;
+        float best = -INFINITY, m = -INFINITY;
+#pragma unroll 8
+        for (int c = tid; c < nch; c += kPickThreads) best = fmaxf(best, cmax[c]);
+        const float2 p0 = tid < g.nb ? part[tid] : make_float2(-INFINITY, 0.f);
+        m = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 1));
+        if ((lane & 1) == 0) s_group[tid >> 1] = m;
+        m = beam_warp_max(m);
+        if (lane == 0) s_top[warp] = m;
+        __syncthreads();
+        float top = s_top[0];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const float m2 = __shfl_xor_sync(0xffffffffu, M_, o);
-            const float mk2 = __shfl_xor_sync(0xffffffffu, MK, o);
-            const double s2 = __shfl_xor_sync(0xffffffffu, S, o);
-            nan |= __shfl_xor_sync(0xffffffffu, nan, o);
-            if (m2 == -INFINITY) continue;
-            if (M_ == -INFINITY) { M_ = m2; MK = mk2; S = s2; continue; }
-            if (mk2 > MK) { S = S * pow2d(MK - mk2) + s2; MK = mk2; }
-            else S += s2 * pow2d(mk2 - MK);
-            M_ = fmaxf(M_, m2);
+        for (int i = 1; i < kPickWarps; ++i) top = fmaxf(top, s_top[i]);
+        const float MK = beam_offset(top, khi);
+        const int want = T > 0.f ? g.K : 1;  // T = 0: all mass on the first argmax
+        {
+            // the want-th largest of the 64 groups' maxima bounds the want-th chunk's from
+            // below; each warp places its own sixteen
+            const float x0 = s_group[lane], x1 = s_group[32 + lane];
+            const float mine = warp < 2 ? x0 : x1;
+            const int first = warp * (GROUPS / kPickWarps);
+#pragma unroll
+            for (int q = 0; q < GROUPS / kPickWarps; ++q) {
+                const int me = first + q;
+                const float y = __shfl_sync(0xffffffffu, mine, me & 31);
+                const unsigned b0 = __ballot_sync(0xffffffffu, x0 > y || (x0 == y && lane < me));
+                const unsigned b1 = __ballot_sync(0xffffffffu, x1 > y || (x1 == y && 32 + lane < me));
+                if (__popc(b0) + __popc(b1) == want - 1 && lane == 0) s_tau = y;
+            }
         }
-        if (nan || M_ == -INFINITY || M_ == INFINITY || (T > 0.f && !(S > 0.0 && S <= DBL_MAX && MK <= FLT_MAX))) {
+        double S = 0.0;
+        {
+            auto add = [&](const float2& p) {
+                S += (double)p.y * (p.x == -INFINITY ? 1.0 : pow2d(beam_offset(p.x, khi) - MK));
+            };
+            add(p0);
+            for (int t = tid + kPickThreads; t < g.nb; t += kPickThreads) add(part[t]);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
+            if (lane == 0) s_sum[warp] = S;
+        }
+        __syncthreads();
+        S = s_sum[0];
+#pragma unroll
+        for (int i = 1; i < kPickWarps; ++i) S += s_sum[i];
+        // (a NaN or +inf makes S NaN; an all -inf batch has sum 0)
+        if (!(top > -INFINITY && top < INFINITY) || S != S || (T > 0.f && !(S > 0.0 && S <= DBL_MAX && MK <= FLT_MAX))) {
             bad = SV_ROW_BAD_LOGITS;
         } else {
-            const double lse = T > 0.f ? ((double)MK + log2(S)) * kLn2 : 0.0;
-            const int want = T > 0.f ? g.K : 1;  // T = 0: all mass on the first argmax
-            const uint2* list = g.list + row * g.nseg * g.K;
-            constexpr int LL = kBeamMaxSegs / 32;  // lists per lane
-            int at[LL];
-            unsigned hv[LL], hi[LL];
-#pragma unroll
-            for (int l = 0; l < LL; ++l) {
-                const int s = l * 32 + lane;
-                at[l] = 0;
-                hv[l] = 0u;  // below every number's order
-                hi[l] = 0xffffffffu;
-                if (s < g.nseg) {
-                    const uint2 h = list[(size_t)s * g.K];
-                    if (h.y != 0xffffffffu) { hv[l] = beam_ord(__uint_as_float(h.x)); hi[l] = h.y; }
-                }
-            }
-            for (int k = 0; k < want; ++k) {
-                unsigned bv = hv[0], bi = hi[0];
-#pragma unroll
-                for (int l = 1; l < LL; ++l)
-                    if (hv[l] > bv || (hv[l] == bv && hi[l] < bi)) { bv = hv[l]; bi = hi[l]; }
-                const unsigned top = __reduce_max_sync(0xffffffffu, bv);
-                if (top == 0u) break;
-                const unsigned ti = __reduce_min_sync(0xffffffffu, bv == top ? bi : 0xffffffffu);
-                if (bv == top && bi == ti) {
-                    const unsigned u = top ^ ((top >> 31) ? 0x80000000u : 0xffffffffu);
-                    const double l = (double)__uint_as_float(u);
-                    s_key[w * g.K + k] = T > 0.f ? (double)sc + (l / (double)T - lse) : (double)sc;
-                    s_tok[w * g.K + k] = (int)ti;
-#pragma unroll
-                    for (int q = 0; q < LL; ++q) {
-                        if (hi[q] == ti) {
-                            hv[q] = 0u;
-                            hi[q] = 0xffffffffu;
-                            if (++at[q] < g.K) {
-                                const uint2 h = list[(size_t)(q * 32 + lane) * g.K + at[q]];
-                                if (h.y != 0xffffffffu) { hv[q] = beam_ord(__uint_as_float(h.x)); hi[q] = h.y; }
-                            }
-                        }
+            // ---- the `want` best chunks (and, meanwhile, the normaliser's logarithm)
+            const float tau = s_tau;
+            if (tid == kPickThreads - 1) s_lse = ((double)MK + log2(S)) * kLn2;
+            if (best >= tau) {
+                for (int c = tid; c < nch; c += kPickThreads) {
+                    const float x = cmax[c];
+                    if (x >= tau && x > -INFINITY) {
+                        const int at = atomicAdd(&s_n, 1);
+                        if (at < kBeamCap) s_cand[at] = beam_key(x, c);
                     }
                 }
-                ++cnt;
+            }
+            __syncthreads();
+            int n = s_n;
+            if (n <= kBeamCap) {
+                if (tid < 4) s_cand[n + tid] = 0ull;
+                __syncthreads();
+                for (int c = tid; c < n; c += kPickThreads) {
+                    const unsigned long long k1 = s_cand[c];
+                    const int rank = pick_rank(s_cand, n, k1);
+                    if (rank < want) s_sel[rank] = (int)(0xffffffffu - (unsigned)k1);
+                    // every logit wanted is at or above the last chosen chunk's maximum (all
+                    // are wanted where the chunks are fewer)
+                    if (rank == want - 1) s_low = beam_unord((unsigned)(k1 >> 32));
+                }
+            } else {  // many equal maxima
+                pick_one_by_one(want, s_tmp,
+                                [&](auto f) {
+                                    for (int c = tid; c < nch; c += kPickThreads) f(beam_key(cmax[c], c));
+                                },
+                                [&](int k, unsigned long long k1) {
+                                    s_sel[k] = (int)(0xffffffffu - (unsigned)k1);
+                                    s_low = beam_unord((unsigned)(k1 >> 32));
+                                });
+            }
+            __syncthreads();
+            // ---- the logits of the chosen chunks
+            const float low = s_low;
+            const unsigned char* base = static_cast<const unsigned char*>(g.logits);
+            const unsigned char* end = base + (size_t)g.B * g.W * g.V * ESZ;
+            const unsigned char* rp = base + (size_t)row * g.V * ESZ;
+            const int vectors = min(n, want) << g.Lsh;
+            // first token of vector t of the chosen
+            auto index = [&](int t) { return t < vectors ? s_sel[t >> g.Lsh] * CH + (t & (L - 1)) * VEC : g.V; };
+            for (int t0 = tid; t0 < vectors; t0 += kPickThreads * NU) {
+                uint4 v[NU];
+#pragma unroll
+                for (int u = 0; u < NU; ++u) v[u] = beam_ld<ESZ, AL>(rp, index(t0 + u * kPickThreads), g.V, end);
+#pragma unroll
+                for (int u = 0; u < NU; ++u) {
+                    float x[VEC];
+                    unpack<ESZ>(v[u], x);
+                    unsigned hit = 0;
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) hit |= (x[e] >= low && x[e] > -INFINITY ? 1u : 0u) << e;
+                    if (hit) {
+                        const int i = index(t0 + u * kPickThreads);
+                        int at = atomicAdd(&s_m, __popc(hit));
+                        do {
+                            const int e = __ffs(hit) - 1, word = e * ESZ / 4;
+                            hit &= hit - 1;
+                            uint32_t q = word == 0 ? v[u].x : (word == 1 ? v[u].y : (word == 2 ? v[u].z : v[u].w));
+                            if (ESZ == 2) q = (e & 1) ? q & 0xffff0000u : q << 16;
+                            if (at < kBeamCap) s_cand[at] = beam_key(__uint_as_float(q), i + e);
+                            ++at;
+                        } while (hit);
+                    }
+                }
+            }
+            __syncthreads();
+            n = s_m;
+            cnt = min(n, want);
+            const double lse = s_lse;
+            auto put = [&](int k, unsigned long long k1) {
+                const double l = (double)beam_unord((unsigned)(k1 >> 32));
+                key[k] = T > 0.f ? (double)sc + (l / (double)T - lse) : (double)sc;
+                tok[k] = (int)(0xffffffffu - (unsigned)k1);
+            };
+            if (n <= kBeamCap) {
+                if (tid < 4) s_cand[n + tid] = 0ull;
+                __syncthreads();
+                for (int c = tid; c < n; c += kPickThreads) {
+                    const unsigned long long k1 = s_cand[c];
+                    const int rank = pick_rank(s_cand, n, k1);
+                    if (rank < want) put(rank, k1);
+                }
+            } else {  // many equal logits
+                pick_one_by_one(want, s_tmp,
+                                [&](auto f) {
+                                    for (int t = tid; t < vectors; t += kPickThreads) {
+                                        const int i = index(t);
+                                        float x[VEC];
+                                        unpack<ESZ>(beam_ld<ESZ, AL>(rp, i, g.V, end), x);
+#pragma unroll
+                                        for (int e = 0; e < VEC; ++e) f(beam_key(x[e], i + e));
+                                    }
+                                },
+                                put);
             }
         }
     }
-    if (lane == 0) { s_cnt[w] = cnt; s_bad[w] = bad; }
+    if (tid == 0) g.row_info[row] = make_int2(cnt, bad);
+    // ---- the sequence's last row to finish joins them
+    if (g.W > 1) {
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) s_last = atomicAdd(g.ticket + b, 1u) == (unsigned)g.W - 1u;
+        __syncthreads();
+        if (!s_last) return;
+        __threadfence();
+    } else {
+        __syncthreads();  // this row is the sequence
+    }
+    const size_t row0 = (size_t)b * g.W;
+    // the keys, as integers of their order, where the candidates' memory is no longer needed
+    const double* keys = g.key + row0 * g.K;
+    const bool fits = g.W * g.K <= kBeamCap;
+    auto ordered = [](double x) {
+        const unsigned long long u = (unsigned long long)__double_as_longlong(x + 0.0);
+        return u ^ ((u >> 63) ? ~0ull : 0x8000000000000000ull);
+    };
+    if (fits)
+        for (int c = tid; c < g.W * g.K; c += kPickThreads) s_cand[c] = ordered(__ldcg(keys + c));
     __syncthreads();
-    if (w != 0) return;
-    // a lane per beam: the K best keys, ties to the lower beam
-    const int have = lane < g.W ? s_cnt[lane] : 0;
-    int p = 0;
+    if (warp != 0) return;
+    // a lane per beam, its list's head in hand (0: none): the K largest heads one by one,
+    // ties to the lower beam
+    const int2 info = lane < g.W ? __ldcg(g.row_info + row0 + lane) : make_int2(0, 0);
+    const unsigned st = __reduce_or_sync(0xffffffffu, (unsigned)info.y);
+    if (g.out_status && lane == 0) g.out_status[b] = (int)(st | (t_ok ? 0u : SV_ROW_BAD_TEMPERATURE));
+    auto head = [&](int p) {
+        if (p >= info.x) return 0ull;
+        return fits ? s_cand[lane * g.K + p] : ordered(__ldcg(keys + lane * g.K + p));
+    };
+    int p = 0, parent = -1, place = 0;  // lane k: the k-th winner
+    unsigned long long now = head(0), after = head(1);
     for (int k = 0; k < g.K; ++k) {
-        unsigned long long o = 0ull;
-        double key = -INFINITY;
-        if (p < have) {
-            key = s_key[lane * g.K + p] + 0.0;
-            const unsigned long long u = (unsigned long long)__double_as_longlong(key);
-            o = u ^ ((u >> 63) ? ~0ull : 0x8000000000000000ull);
+        const unsigned long long top = beam_warp_max64(now);
+        if (top == 0ull) break;
+        const int who = __ffs(__ballot_sync(0xffffffffu, now == top)) - 1;
+        const int at = __shfl_sync(0xffffffffu, p, who);
+        if (lane == k) {
+            parent = who;
+            place = at;
         }
-        const unsigned hi = (unsigned)(o >> 32), th = __reduce_max_sync(0xffffffffu, hi);
-        const unsigned lo = hi == th ? (unsigned)o : 0u, tl = __reduce_max_sync(0xffffffffu, lo);
-        const unsigned who = __ballot_sync(0xffffffffu, p < have && hi == th && (unsigned)o == tl);
-        const size_t at = (size_t)b * g.K + k;
-        if (who == 0u) {
-            if (lane == 0) { g.out_parent[at] = -1; g.out_token[at] = -1; g.out_score[at] = -INFINITY; }
-        } else if (lane == __ffs(who) - 1) {
-            g.out_parent[at] = lane;
-            g.out_token[at] = s_tok[lane * g.K + p];
-            g.out_score[at] = (float)key;
+        if (lane == who) {
             ++p;
+            now = after;
+            after = head(p + 1);
         }
     }
-    if (g.out_status) {
-        int st = __reduce_or_sync(0xffffffffu, lane < g.W ? (unsigned)s_bad[lane] : 0u);
-        if (!t_ok) st |= SV_ROW_BAD_TEMPERATURE;
-        if (lane == 0) g.out_status[b] = st;
+    if (lane < g.K) {
+        const size_t at = (size_t)b * g.K + lane;
+        g.out_parent[at] = parent;
+        g.out_token[at] = parent < 0 ? -1 : __ldcg(g.tok + (row0 + parent) * g.K + place);
+        g.out_score[at] = parent < 0 ? -INFINITY : (float)__ldcg(keys + parent * g.K + place);
     }
 }
 

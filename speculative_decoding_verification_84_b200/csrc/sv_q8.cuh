@@ -6,10 +6,9 @@
 // even), scale = a / (127 rms), rms = sqrt(mean(s^2) + eps).  The norm's factor
 // cancels out of q, so one reduction gives everything: sum s^2 and max |p|.  Sums
 // are fp32 (fp64 where they leave its range), q is the integer that the formula
-// gives in fp64: fp32 decides all values but those within 1e-4 of a half (its
-// error is below 6 * 2^-24 * 127 = 5e-5), and those are decided in fp64, against
-// the fp64 maximum.  A second pair of roundings would make such a value depend on
-// the order of the row's sum.
+// gives in fp64: fp32 decides all values but those within 6e-5 of a half (seven
+// roundings at most, 7 * 2^-24 * 127 = 5.3e-5), and those are decided in fp64,
+// against the fp64 maximum.
 //   sv_q8_rows       a row in registers, blockDim.x threads a row
 //   sv_q8_rows_long  rows beyond that: read three times, fp64 throughout
 //
@@ -59,6 +58,25 @@ __device__ __forceinline__ void q8_st1(void* p, size_t i, float v)
 {
     if (ESZ == 4) static_cast<float*>(p)[i] = v;
     else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+}
+
+// VEC elements (16 bytes, or one)
+template <int ESZ, int VEC>
+__device__ __forceinline__ void q8_st(void* p, size_t i, const float* v)
+{
+    if (VEC == 1) {
+        q8_st1<ESZ>(p, i, v[0]);
+    } else if (ESZ == 2) {
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[(2 * e) % VEC], v[(2 * e + 1) % VEC]);
+            o[e] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        *reinterpret_cast<uint4*>(static_cast<char*>(p) + i * ESZ) = make_uint4(o[0], o[1], o[2], o[3]);
+    } else {
+        *reinterpret_cast<float4*>(static_cast<char*>(p) + i * ESZ) = make_float4(v[0], v[1 % VEC], v[2 % VEC], v[3 % VEC]);
+    }
 }
 
 __device__ __forceinline__ double q8_warp_sum(double v)
@@ -116,195 +134,342 @@ __global__ void __launch_bounds__(1024) sv_q8_rows_long(Q8RowsArgs g)
     }
 }
 
-// NV pieces of VEC elements a thread (VEC x ESZ = 16 bytes, or VEC = 1 for rows
-// that start at no vector boundary); blockDim.x threads a row, and blockDim.y rows
-// a CTA when blockDim.x is one warp (no barrier then).
-template <int ESZ, int VEC, int NV>
-__global__ void __launch_bounds__(1024) sv_q8_rows(Q8RowsArgs g)
+__device__ __forceinline__ void q8_cp16(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// max(m, |a|, |b|); a NaN stays
+__device__ __forceinline__ float q8_max3(float m, float a, float b)
+{
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(m), "f"(a), "f"(b));
+    return d;
+}
+
+// A 16-byte vector's elements as packed fp32 pairs.
+template <int ESZ, int P>
+__device__ __forceinline__ void q8_pairs(const uint4& v, unsigned long long (&p)[P])
+{
+    float x[16 / ESZ];
+    unpack<ESZ>(v, x);
+#pragma unroll
+    for (int e = 0; e < P; ++e) p[e] = pack2(x[2 * e], x[2 * e + 1]);
+}
+
+constexpr int kQ8RowSlots = 3;
+
+// NV pieces of VEC elements a thread: 16-byte vectors, or (VEC = 1) elements, for rows
+// that start at no vector boundary.  blockDim.x threads a row, and blockDim.y rows
+// a CTA when blockDim.x is one warp (no barrier then); CTAs walk the rows.
+//
+// Vectors come through shared memory by asynchronous copies, the next row's on the way
+// while this one is worked on (each thread copies what it reads itself, so no barrier
+// belongs to it).  The row's products stay in registers over the reduction, two
+// to an instruction throughout.  The fp64 maximum is formed only by a warp that holds
+// a value near a half, from the part of the row that holds the fp32 maximum, so the
+// row has one barrier; a warp can be one row ahead of another, hence three slots and
+// two sets of partials.  out_sum, which may be an input, is written last.
+template <int ESZ, int VEC, int NV, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NV <= 2 || (VEC == 1 && NV <= 8) ? 4 : 3) : 1) sv_q8_rows(Q8RowsArgs g)
 {
     static_assert(VEC == 1 || VEC * ESZ == 16, "a piece is an element or a 16-byte vector");
-    __shared__ float s_ss[32];
-    __shared__ unsigned s_pm[32];
-    __shared__ double s_dm[32];
-    const int row = blockIdx.x * blockDim.y + threadIdx.y;
-    if (row >= g.M) return;  // only where a row is one warp
+    constexpr int P = VEC > 1 ? VEC / 2 : 1;   // packed pairs of a vector
+    extern __shared__ __align__(16) unsigned char q8_rows_dyn[];  // VEC > 1: [slots][x, r][NV][threads] vectors
+    __shared__ float s_ss[2][32];
+    __shared__ unsigned s_pm[2][32];
+    __shared__ double s_sd[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x, nw = nthr >> 5;
-    const size_t base = (size_t)row * g.d;
-
-    // every load first (sum may be written over x or r)
-    uint4 xv[VEC > 1 ? NV : 1], rv[VEC > 1 ? NV : 1], wv[VEC > 1 ? NV : 1];
-    float x1[VEC > 1 ? 1 : NV], r1[VEC > 1 ? 1 : NV], w1[VEC > 1 ? 1 : NV];
+    const int all = nthr * blockDim.y, inputs = g.r ? 2 : 1;
+    const int stride = gridDim.x * blockDim.y;
     const uint32_t one = ESZ == 2 ? 0x3f803f80u : 0x3f800000u;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int i = (j * nthr + tid) * VEC;
-        const bool in = i < g.d;
-        if (VEC > 1) {
-            xv[j] = in ? *reinterpret_cast<const uint4*>(static_cast<const char*>(g.x) + (base + i) * ESZ) : make_uint4(0, 0, 0, 0);
-            rv[j] = (in && g.r) ? *reinterpret_cast<const uint4*>(static_cast<const char*>(g.r) + (base + i) * ESZ)
-                                : make_uint4(0, 0, 0, 0);
-            wv[j] = (in && g.w) ? __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(g.w) + (size_t)i * ESZ))
-                                : make_uint4(one, one, one, one);
-        } else {
-            x1[j] = in ? q8_ld1<ESZ>(g.x, base + i) : 0.f;
-            r1[j] = (in && g.r) ? q8_ld1<ESZ>(g.r, base + i) : 0.f;
-            w1[j] = (in && g.w) ? q8_ld1<ESZ>(g.w, i) : 1.f;
-        }
-    }
-    auto get = [&](int j, float* x, float* r, float* w) {
-        if (VEC > 1) {
-            unpack<ESZ>(xv[j], x);
-            unpack<ESZ>(rv[j], r);
-            unpack<ESZ>(wv[j], w);
-        } else {
-            x[0] = x1[j];
-            r[0] = r1[j];
-            w[0] = w1[j];
-        }
-    };
-    float ss = 0.f;
-    unsigned tpm = 0;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        float x[VEC], r[VEC], w[VEC];
-        get(j, x, r, w);
-        const int i = (j * nthr + tid) * VEC;
-        float s[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            s[e] = x[e] + r[e];
-            ss = fmaf(s[e], s[e], ss);
-            tpm = max(tpm, __float_as_uint(s[e] * w[e]) & 0x7fffffffu);
-        }
-        if (g.sum && i < g.d) {
-            if (VEC > 1 && ESZ == 2) {
-                uint32_t o[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(s[(2 * e) % VEC], s[(2 * e + 1) % VEC]);
-                    o[e] = *reinterpret_cast<const uint32_t*>(&h);
-                }
-                *reinterpret_cast<uint4*>(static_cast<char*>(g.sum) + (base + i) * ESZ) = make_uint4(o[0], o[1], o[2], o[3]);
-            } else if (VEC > 1) {
-                *reinterpret_cast<float4*>(static_cast<char*>(g.sum) + (base + i) * ESZ) =
-                    make_float4(s[0], s[1 % VEC], s[2 % VEC], s[3 % VEC]);
-            } else {
-                q8_st1<ESZ>(g.sum, base + i, s[0]);
-            }
-        }
-    }
-    // sum s^2 and max |p| (as bits: NaN and inf order above every number)
-    unsigned pm = __reduce_max_sync(0xffffffffu, tpm);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (nw > 1) {
-        if (lane == 0) { s_ss[warp] = ss; s_pm[warp] = pm; }
-        __syncthreads();
-        ss = lane < nw ? s_ss[lane] : 0.f;
-        pm = __reduce_max_sync(0xffffffffu, lane < nw ? s_pm[lane] : 0u);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    }
-    const bool bad = pm >= 0x7f800000u;
-    const float pmf = __uint_as_float(pm);
-    const bool tiny = pmf < 0x1p-100f;  // 127 / pmf, or the products themselves, leave fp32: all in fp64
-    // the maximum in fp64, over the values that reach the fp32 one to 2^-20
-    const float thr = tiny ? 0.f : pmf * (1.f - 0x1p-20f);
-    double dm = 0.0;
-    if (__uint_as_float(tpm) >= thr && !bad) {
+    uint4* const slots = reinterpret_cast<uint4*>(q8_rows_dyn) + threadIdx.y * nthr;
+
+    auto copy = [&](int row, int slot) {
+        if (VEC == 1) return;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            float x[VEC], r[VEC], w[VEC];
-            get(j, x, r, w);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                if (fabsf((x[e] + r[e]) * w[e]) >= thr) dm = fmax(dm, fabs(((double)x[e] + (double)r[e]) * (double)w[e]));
+            const int i = (j * nthr + tid) * VEC;
+            if (i < g.d) {
+                uint4* to = slots + (slot * inputs * NV + j) * all + tid;
+                q8_cp16(lr_smem(to), static_cast<const char*>(g.x) + ((size_t)row * g.d + i) * ESZ);
+                if (g.r) q8_cp16(lr_smem(to + NV * all), static_cast<const char*>(g.r) + ((size_t)row * g.d + i) * ESZ);
+            }
         }
-    }
-    dm = q8_warp_max(dm);
-    if (nw > 1) {
-        if (lane == 0) s_dm[warp] = dm;
-        __syncthreads();
-        dm = q8_warp_max(lane < nw ? s_dm[lane] : 0.0);
-    }
-    // the norm; a sum of squares outside fp32's comfortable range is taken again in fp64
-    double ms = 1.0;
-    if (g.norm) {
-        ms = (double)ss / g.d + (double)g.eps;
-        if (!bad && (!(ss <= 0x1p120f) || ms < 0x1p-80)) {
-            double sd = 0.0;
+    };
+    int row = blockIdx.x * blockDim.y + threadIdx.y, slot = 0, set = 0;
+    if (row < g.M) copy(row, 0);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    for (; row < g.M; row += stride, slot = slot == kQ8RowSlots - 1 ? 0 : slot + 1, set ^= 1) {
+        const size_t base = (size_t)row * g.d;
+        // element e of piece j of thread t, in fp64: s, and s w
+        auto sum64 = [&](int j, int t, int e) {
+            const int i = (j * nthr + t) * VEC + e;
+            if (VEC > 1) {
+                const void* at = slots + (slot * inputs * NV + j) * all + t;
+                const double x = q8_ld1<ESZ>(at, e);
+                return g.r ? x + (double)q8_ld1<ESZ>(static_cast<const uint4*>(at) + NV * all, e) : x;
+            }
+            const double x = q8_ld1<ESZ>(g.x, base + i);
+            return g.r ? x + (double)q8_ld1<ESZ>(g.r, base + i) : x;
+        };
+        auto prod64 = [&](int j, int t, int e) {
+            return sum64(j, t, e) * (g.w ? (double)q8_ld1<ESZ>(g.w, (j * nthr + t) * VEC + e) : 1.0);
+        };
+        unsigned long long p2[VEC > 1 ? NV * P : 1], s2[VEC > 1 ? NV * P : 1];
+        uint32_t total[VEC > 1 && ESZ == 2 ? NV * P : 1];  // bf16: the sums as they are stored
+        float p1[VEC > 1 ? 1 : NV], s1[VEC > 1 ? 1 : NV];
+        float tm = 0.f, ss;
+        if (VEC > 1) {
+            if (row < g.M - stride) copy(row + stride, slot == kQ8RowSlots - 1 ? 0 : slot + 1);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            unsigned long long acc[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                float x[VEC], r[VEC], w[VEC];
-                get(j, x, r, w);
+                const int i = (j * nthr + tid) * VEC;
+                uint4 x = make_uint4(0, 0, 0, 0), r = x, c = make_uint4(one, one, one, one);
+                if (i < g.d) {
+                    const uint4* at = slots + (slot * inputs * NV + j) * all + tid;
+                    x = *at;
+                    if (g.r) r = at[NV * all];
+                    if (g.w) c = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(g.w) + (size_t)i * ESZ));
+                }
+                unsigned long long a[P], b[P], w[P];
+                q8_pairs<ESZ>(x, a);
+                if (g.r) {
+                    q8_pairs<ESZ>(r, b);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const double s = (double)x[e] + (double)r[e];
-                    sd += s * s;
+                    for (int e = 0; e < P; ++e) a[e] = add2(a[e], b[e]);
+                }
+                q8_pairs<ESZ>(c, w);
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    float u, v;
+                    acc[j & 1] = fma2(a[e], a[e], acc[j & 1]);
+                    p2[j * P + e] = mul2(a[e], w[e]);
+                    unpack2(p2[j * P + e], u, v);
+                    tm = q8_max3(tm, u, v);
+                    if (ESZ == 4) {
+                        s2[j * P + e] = a[e];
+                    } else {
+                        unpack2(a[e], u, v);
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(u, v);
+                        total[j * P + e] = *reinterpret_cast<const uint32_t*>(&h);
+                    }
                 }
             }
+            float u, v;
+            unpack2(add2(acc[0], acc[1]), u, v);
+            ss = u + v;
+        } else {
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int i = j * nthr + tid;
+                const bool in = i < g.d;
+                s1[j] = in ? q8_ld1<ESZ>(g.x, base + i) : 0.f;
+                if (in && g.r) s1[j] += q8_ld1<ESZ>(g.r, base + i);
+                p1[j] = s1[j] * ((in && g.w) ? q8_ld1<ESZ>(g.w, i) : 1.f);
+                acc[j & 3] = fmaf(s1[j], s1[j], acc[j & 3]);
+                tm = q8_max3(tm, p1[j], 0.f);
+            }
+            ss = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+        }
+        // sum s^2 and max |p| (as bits: NaN and inf order above every number)
+        unsigned pm = __reduce_max_sync(0xffffffffu, __float_as_uint(tm));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        bool large = !(ss <= 0x1p110f), small = ss < 0x1p-60f && g.eps < 0x1p-60f;
+        if (nw > 1) {
+            if (lane == 0) { s_ss[set][warp] = ss; s_pm[set][warp] = pm; }
+            __syncthreads();
+            const float other = lane < nw ? s_ss[set][lane] : 0.f;
+            pm = __reduce_max_sync(0xffffffffu, lane < nw ? s_pm[set][lane] : 0u);
+            large = __any_sync(0xffffffffu, !(other <= 0x1p110f));
+            small = g.eps < 0x1p-60f && __all_sync(0xffffffffu, other < 0x1p-60f);
+            if (warp == 0 || g.normed) {
+                ss = other;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            }
+        }
+        const bool bad = pm >= 0x7f800000u;
+        const float pmf = __uint_as_float(pm);
+        const bool tiny = pmf < 0x1p-100f;  // 127 / pmf, or the products themselves, leave fp32: all in fp64
+        // a sum of squares outside fp32's comfortable range is taken again in fp64
+        double sd = 0.0;
+        const bool again = g.norm && !bad && (large || small);
+        if (again) {
+#pragma unroll 1
+            for (int j = 0; j < NV; ++j)
+                if ((j * nthr + tid) * VEC < g.d)
+#pragma unroll 1
+                    for (int e = 0; e < VEC; ++e) {
+                        const double s = sum64(j, tid, e);
+                        sd += s * s;
+                    }
             sd = q8_warp_sum(sd);
             if (nw > 1) {
-                __syncthreads();  // s_dm is read
-                if (lane == 0) s_dm[warp] = sd;
+                if (lane == 0) s_sd[warp] = sd;
                 __syncthreads();
-                sd = q8_warp_sum(lane < nw ? s_dm[lane] : 0.0);
+                sd = q8_warp_sum(lane < nw ? s_sd[lane] : 0.0);
+                __syncthreads();  // the next row may write s_sd
             }
-            ms = sd / g.d + (double)g.eps;
         }
-    }
-    const bool zero = !(dm > 0.0);
-    if (tid == 0) g.scale[row] = bad ? NAN : (zero ? 0.f : (float)(dm / (127.0 * sqrt(ms))));
-    const float k = 127.f / pmf;
-    const bool wide = tiny || ms < 0x1p-200 || ms > 0x1p200;  // 1 / rms, or p, leaves fp32
-    float inv = 0.f;
-    if (g.normed) inv = bad ? NAN : (zero ? 0.f : (float)(1.0 / sqrt(ms)));
+        // the integers
+        const float k = 127.f * __frcp_rn(pmf);
+        uint32_t o[VEC > 1 ? NV * P / 2 : NV];
+        float far = 0.f;  // the largest distance from an integer
+        if (VEC > 1) {
+            const unsigned long long K2 = pack2(k, k), magic = pack2(0x1.8p23f, 0x1.8p23f);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int i = (j * nthr + tid) * VEC;
-        if (i >= g.d) continue;
-        float x[VEC], r[VEC], w[VEC], y[VEC];
-        get(j, x, r, w);
-        int q[VEC];
+            for (int e = 0; e < NV * P; e += 2) {
+                uint32_t lo[2], hi[2];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const float p = (x[e] + r[e]) * w[e];
-            const float t = p * k, n = rintf(t);
-            q[e] = (int)n;
-            if (fabsf(t - n) > 0.4999f || tiny) {
-                const double pd = ((double)x[e] + (double)r[e]) * (double)w[e];
-                q[e] = zero ? 0 : (int)rint(pd * 127.0 / dm);
-            }
-            if (bad) q[e] = 0;
-            y[e] = p * inv;
-            if (g.normed && wide && !bad && !zero) y[e] = (float)(((double)x[e] + (double)r[e]) * (double)w[e] / sqrt(ms));
-        }
-        int8_t* qo = g.q + (size_t)row * g.ldq + i;
-        if (VEC == 1) {
-            qo[0] = (int8_t)q[0];
-        } else {
-            uint32_t o[VEC > 4 ? 2 : 1];
-#pragma unroll
-            for (int h = 0; h < (VEC > 4 ? 2 : 1); ++h)
-                o[h] = (uint32_t)(q[(4 * h) % VEC] & 255) | (uint32_t)(q[(4 * h + 1) % VEC] & 255) << 8 |
-                       (uint32_t)(q[(4 * h + 2) % VEC] & 255) << 16 | (uint32_t)(q[(4 * h + 3) % VEC] & 255) << 24;
-            if (VEC > 4) *reinterpret_cast<uint2*>(qo) = make_uint2(o[0], o[VEC > 4 ? 1 : 0]);
-            else *reinterpret_cast<uint32_t*>(qo) = o[0];
-        }
-        if (g.normed) {
-            if (VEC > 1 && ESZ == 2) {
-                uint32_t o[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(y[(2 * e) % VEC], y[(2 * e + 1) % VEC]);
-                    o[e] = *reinterpret_cast<const uint32_t*>(&h);
+                for (int h = 0; h < 2; ++h) {
+                    // adding 1.5 * 2^23 rounds to an integer, ties to even, in the low bits
+                    const unsigned long long t = mul2(p2[e + h], K2), m = add2(t, magic);
+                    float u, v;
+                    unpack2(sub2(t, sub2(m, magic)), u, v);
+                    far = q8_max3(far, u, v);
+                    lo[h] = (uint32_t)m;
+                    hi[h] = (uint32_t)(m >> 32);
                 }
-                *reinterpret_cast<uint4*>(static_cast<char*>(g.normed) + (base + i) * ESZ) = make_uint4(o[0], o[1], o[2], o[3]);
-            } else if (VEC > 1) {
-                *reinterpret_cast<float4*>(static_cast<char*>(g.normed) + (base + i) * ESZ) =
-                    make_float4(y[0], y[1 % VEC], y[2 % VEC], y[3 % VEC]);
+                o[e / 2] = __byte_perm(__byte_perm(lo[0], hi[0], 0x0040), __byte_perm(lo[1], hi[1], 0x0040), 0x5410);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const float t = p1[j] * k, n = rintf(t);
+                far = q8_max3(far, t - n, 0.f);
+                o[j] = (uint32_t)(int)n;
+            }
+        }
+        int8_t* qrow = g.q + (size_t)row * g.ldq;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int i = (j * nthr + tid) * VEC;
+            if (i >= g.d) continue;
+            if (VEC == 1) {
+                qrow[i] = bad ? (int8_t)0 : (int8_t)o[j];
+            } else if (VEC > 4) {
+                *reinterpret_cast<uint2*>(qrow + i) = bad ? make_uint2(0, 0) : make_uint2(o[j * P / 2], o[j * P / 2 + (P > 2 ? 1 : 0)]);
             } else {
-                q8_st1<ESZ>(g.normed, base + i, y[0]);
+                *reinterpret_cast<uint32_t*>(qrow + i) = bad ? 0u : o[j * P / 2];
+            }
+        }
+        // values near a half: in fp64, and written again
+        const bool near = !bad && (tiny || far > 0.49994f);
+        double dm = pmf;  // the maximum, as exactly as it is needed
+        if (__any_sync(0xffffffffu, near)) {
+            unsigned todo = 0;  // elements j * VEC + e
+            if (near) {
+                unsigned long long K2 = pack2(k, k), magic = pack2(0x1.8p23f, 0x1.8p23f);
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+#pragma unroll
+                    for (int e = 0; e < VEC; e += 2) {
+                        float u = 0.f, v = 0.f;
+                        if (VEC > 1) {
+                            const unsigned long long t = mul2(p2[j * P + e / 2], K2);
+                            unpack2(sub2(t, sub2(add2(t, magic), magic)), u, v);
+                        } else {
+                            const float t = p1[j] * k;
+                            u = t - rintf(t);
+                        }
+                        if (tiny || fabsf(u) > 0.49994f) todo |= 1u << (j * VEC + e);
+                        if (VEC > 1 && (tiny || fabsf(v) > 0.49994f)) todo |= 2u << (j * VEC + e);
+                    }
+            }
+            // first against the fp32 maximum, good to 2^-23 (1.6e-5 of a value up to 127); what
+            // that leaves open needs the fp64 maximum, unless the products are exact in fp32
+            const bool exact = !tiny && !g.r && (ESZ == 2 || !g.w);
+            for (int round = 0; round < 2; ++round) {
+                unsigned open = 0;
+                for (unsigned left = todo; left; left &= left - 1) {
+                    const int at = __ffs(left) - 1, j = at / VEC, e = at % VEC, i = (j * nthr + tid) * VEC + e;
+                    if (i >= g.d) continue;
+                    const double t = dm > 0.0 ? prod64(j, tid, e) * 127.0 / dm : 0.0, n = rint(t);
+                    if (round == 0 && !exact && (tiny || fabs(t - n) > 0.49998)) open |= 1u << at;
+                    else qrow[i] = (int8_t)(int)n;
+                }
+                todo = open;
+                if (round || !__any_sync(0xffffffffu, todo != 0u)) break;
+                // the fp64 maximum: over the values that reach the fp32 one to 2^-20, in the
+                // parts of the row that hold one
+                const float thr = tiny ? 0.f : pmf * (1.f - 0x1p-20f);
+                dm = 0.0;
+                __syncwarp();  // one warp a row: the other lanes' copies
+                for (int t = 0; t < nw; ++t) {
+                    if (nw > 1 && !(__uint_as_float(s_pm[set][t]) >= thr)) continue;
+#pragma unroll 1
+                    for (int j = 0; j < NV; ++j) {
+                        const int i = (j * nthr + 32 * t + lane) * VEC;
+                        if (i >= g.d) continue;
+                        unsigned hit = 0;
+                        if (VEC > 1) {
+                            const uint4* at = slots + (slot * inputs * NV + j) * all + 32 * t + lane;
+                            const uint4 c = g.w ? __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(g.w) + (size_t)i * ESZ))
+                                                : make_uint4(one, one, one, one);
+                            float x[16 / ESZ], r[16 / ESZ], w[16 / ESZ];
+                            unpack<ESZ>(at[0], x);
+                            unpack<ESZ>(g.r ? at[NV * all] : make_uint4(0, 0, 0, 0), r);
+                            unpack<ESZ>(c, w);
+#pragma unroll
+                            for (int e = 0; e < VEC; ++e) hit |= (fabsf((x[e] + r[e]) * w[e]) >= thr ? 1u : 0u) << e;
+                        } else {
+                            hit = fabs(prod64(j, 32 * t + lane, 0)) >= (double)thr ? 1u : 0u;
+                        }
+                        for (; hit; hit &= hit - 1) dm = fmax(dm, fabs(prod64(j, 32 * t + lane, __ffs(hit) - 1)));
+                    }
+                }
+                dm = q8_warp_max(dm);
+            }
+        }
+        const double ms = !g.norm ? 1.0 : (again ? sd : (double)ss) / g.d + (double)g.eps;  // by all where g.normed, else by warp 0
+        if (tid == 0) g.scale[row] = bad ? NAN : (dm > 0.0 ? (float)(dm / (127.0 * sqrt(ms))) : 0.f);
+        float inv = 0.f;
+        bool wide = false;
+        if (g.normed) {
+            wide = !bad && (tiny || ms < 0x1p-200 || ms > 0x1p200);  // 1 / rms, or p, leaves fp32
+            inv = bad ? NAN : (ms > 0.0 ? (float)(1.0 / sqrt(ms)) : 0.f);
+        }
+        if (VEC == 1 && nw > 1 && g.sum) __syncthreads();  // another warp may still read inputs of this one's
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int i = (j * nthr + tid) * VEC;
+            if (i >= g.d) continue;
+            if (g.normed) {
+                if (wide) {
+#pragma unroll 1
+                    for (int e = 0; e < VEC; ++e) q8_st1<ESZ>(g.normed, base + i + e, ms > 0.0 ? (float)(prod64(j, tid, e) / sqrt(ms)) : 0.f);
+                } else {
+                    float y[VEC];
+                    if (VEC > 1) {
+#pragma unroll
+                        for (int e = 0; e < P; ++e) unpack2(p2[j * P + e], y[(2 * e) % VEC], y[(2 * e + 1) % VEC]);
+                    } else {
+                        y[0] = p1[j];
+                    }
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) y[e] *= inv;
+                    q8_st<ESZ, VEC>(g.normed, base + i, y);
+                }
+            }
+            if (g.sum) {
+                if (VEC == 1) {
+                    q8_st1<ESZ>(g.sum, base + i, s1[j]);
+                } else if (ESZ == 2) {
+                    *reinterpret_cast<uint4*>(static_cast<char*>(g.sum) + (base + i) * ESZ) =
+                        make_uint4(total[(j * P) % (NV * P)], total[(j * P + 1) % (NV * P)], total[(j * P + 2) % (NV * P)],
+                                   total[(j * P + 3) % (NV * P)]);
+                } else {
+                    ulonglong2 t;
+                    t.x = s2[j * P];
+                    t.y = s2[j * P + P - 1];
+                    *reinterpret_cast<ulonglong2*>(static_cast<char*>(g.sum) + (base + i) * ESZ) = t;
+                }
             }
         }
     }
