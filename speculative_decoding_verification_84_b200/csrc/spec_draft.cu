@@ -192,12 +192,15 @@ bool beam_plan(int B, int W, int V, int K, sv_dtype dt, BeamPlan* p)
 template <int ESZ, bool AL>
 cudaError_t beam_go(const BeamArgs& g, cudaStream_t st)
 {
-    // one span of batches per resident warp
-    const long long batches = (long long)g.B * g.W * g.nb, warps = kBeamThreads / 32;
-    const long long per = cdiv(batches, (long long)device_sm_count() * 4 * warps);
-    if (per > 0x7fffffffLL) return cudaErrorInvalidValue;
-    sv_beam_rows<ESZ, AL><<<(unsigned)cdiv(cdiv(batches, per), warps), kBeamThreads, 0, st>>>(g, (int)per);
-    cudaError_t e = cudaGetLastError();
+    // one span of batches per resident warp (three CTAs of eight warps an SM), in smaller
+    // CTAs where the batches are few, to reach every SM
+    const long long batches = (long long)g.B * g.W * g.nb, sms = device_sm_count();
+    const long long spans = std::min<long long>(batches, sms * 3 * (kBeamThreads / 32)), warps = std::min<long long>(kBeamThreads / 32, cdiv(spans, sms));
+    static std::atomic<bool> ready[kMaxDevices];
+    cudaError_t e = allow_smem(sv_beam_rows<ESZ, AL>, kBeamWarpBytes * (kBeamThreads / 32), ready);
+    if (e != cudaSuccess) return e;
+    sv_beam_rows<ESZ, AL><<<(unsigned)cdiv(spans, warps), (unsigned)(32 * warps), (size_t)(kBeamWarpBytes * warps), st>>>(g, (int)spans);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(g.B * g.W));

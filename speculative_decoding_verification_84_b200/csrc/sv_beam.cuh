@@ -9,9 +9,9 @@
 // beam the keys order as the logits do, whatever its normaliser, and a row's K
 // best logits lie in the K chunks of largest maximum (ties: the earlier chunk, which
 // holds the smaller tokens).  So the pass over the logits selects nothing:
-//   sv_beam_rows   every warp walks a span of the rows: per batch of 4 vectors a
+//   sv_beam_rows   every warp walks a span of the rows: per batch of 8 vectors a
 //                  lane (offset, sum of exponentials), per chunk (L lanes of one
-//                  vector) its maximum.  No barrier, no shared memory.
+//                  vector) its maximum.  No barrier.
 //   sv_beam_pick   one CTA per row: the normaliser in fp64; the K best chunks, of
 //                  which it reads the logits again (K L vectors, from L2); the
 //                  logits at or above the K-th chunk's maximum (about K), ranked
@@ -33,10 +33,11 @@
 namespace sv {
 
 constexpr int kBeamThreads = 256;
-constexpr int kBeamNV = 4;          // vectors a lane and batch
+constexpr int kBeamNV = 8;          // vectors a lane and batch
 constexpr int kPickThreads = 128;
 constexpr int kPickWarps = kPickThreads / 32;
-constexpr int kBeamCap = 512;       // candidates of a row
+constexpr int kBeamCap = 1024;      // candidates of a row, and a sequence's W K keys
+constexpr int kPickChunks = 64;     // chunks a row is looked for in without choosing among them
 
 struct BeamArgs {
     const void* logits;        // [B][W][V]
@@ -56,6 +57,8 @@ struct BeamArgs {
     int B, W, V, K, nb, Lsh;   // chunks of 2^Lsh lanes
     int pad_token;
 };
+
+__device__ __forceinline__ uint32_t beam_smem(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
 __device__ __forceinline__ bool beam_t_ok(float T) { return T == 0.f || (T >= SV_TEMPERATURE_MIN && T <= FLT_MAX); }
 
@@ -152,66 +155,139 @@ __device__ __forceinline__ unsigned long long beam_warp_max64(unsigned long long
     return (unsigned long long)hi << 32 | lo;
 }
 
-// AL: every row starts on a 16-byte boundary (its length is then whole vectors).
+// Bytes of shared memory a warp of sv_beam_rows needs: two batches, and the block that
+// an unaligned row's last vector reaches into.
+constexpr int kBeamSlot = kBeamNV * 32 + 1;
+constexpr int kBeamWarpBytes = 2 * kBeamSlot * 16;
+
+// AL: every row starts on a 16-byte boundary (its length is then whole vectors);
+// otherwise a vector comes from the two 16-byte blocks it lies in.  Only blocks that
+// hold an element of the row are read, and no byte past the logits' end.  The next
+// batch's blocks are copied to the warp's shared memory while this one is worked on;
+// nothing is shared between warps.
 template <int ESZ, bool AL>
-__global__ void __launch_bounds__(kBeamThreads, 4) sv_beam_rows(BeamArgs g, int per_warp)
+__global__ void __launch_bounds__(kBeamThreads, 3) sv_beam_rows(BeamArgs g, int spans)
 {
-    constexpr int VEC = 16 / ESZ, NV = kBeamNV;
+    constexpr int VEC = 16 / ESZ, NV = kBeamNV, STEP = NV * 32 * VEC;  // tokens of a batch
+    constexpr uint32_t ninf = ESZ == 2 ? 0xff80ff80u : 0xff800000u;
+    extern __shared__ __align__(16) unsigned char beam_rows_dyn[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rows = g.B * g.W;
-    const long long first = ((long long)blockIdx.x * (kBeamThreads / 32) + (threadIdx.x >> 5)) * per_warp;
-    int left = (int)max(0ll, min((long long)per_warp, (long long)rows * g.nb - first));
+    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < g.B; i += gridDim.x * blockDim.x) g.ticket[i] = 0u;
+    // this warp's span of the rows' batches
+    const long long span = (long long)blockIdx.x * (blockDim.x >> 5) + warp, batches = (long long)rows * g.nb;
+    if (span >= spans) return;
+    const long long first = span * batches / spans;
+    int left = (int)((span + 1) * batches / spans - first);
     int row = (int)(first / g.nb), batch = (int)(first % g.nb);
     const unsigned char* base = static_cast<const unsigned char*>(g.logits);
     const unsigned char* end = base + (size_t)rows * g.V * ESZ;
     const int L = 1 << g.Lsh, cpv = 32 >> g.Lsh;  // lanes of a chunk, chunks of a warp's vector
-    for (int i = blockIdx.x * kBeamThreads + threadIdx.x; i < g.B; i += gridDim.x * kBeamThreads) g.ticket[i] = 0u;
-    if (left == 0) return;
+    uint4* const slots = reinterpret_cast<uint4*>(beam_rows_dyn) + warp * 2 * kBeamSlot;
 
-    // the row of batch `left`: whether any candidate comes from its logits
-    float T = 1.f;
-    auto look = [&](int r) {
+    // a row's temperature, and whether any candidate comes from its logits
+    auto look = [&](int r, float& T) {
         T = __ldg(g.temperature + r / g.W);
         const float sc = __ldg(g.score + r);
         return beam_t_ok(T) && sc > -INFINITY && sc < INFINITY && !(g.frozen && __ldg(g.frozen + r));
     };
-    auto load = [&](int r, int bt, uint4 (&v)[NV]) {
+    auto copy = [&](int r, int bt, int slot) {
         const unsigned char* rp = base + (size_t)r * g.V * ESZ;
+        const unsigned sh = AL ? 0u : (unsigned)(reinterpret_cast<uintptr_t>(rp) & 15u);
+        const unsigned char* p = rp - sh + (size_t)(bt * NV * 32 + lane) * 16;
+        const uint32_t to = beam_smem(slots + slot * kBeamSlot + lane);
+        if ((bt + 1) * STEP <= g.V && (AL || p - lane * 16 + (NV * 32 + 1) * 16 <= end)) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) v[j] = beam_ld<ESZ, AL>(rp, ((bt * NV + j) * 32 + lane) * VEC, g.V, end);
+            for (int j = 0; j < NV; ++j)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + j * 512), "l"(p + j * 512) : "memory");
+            if (!AL && lane == 0)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + NV * 512), "l"(p + NV * 512) : "memory");
+        } else {
+            const unsigned char* stop = rp + (size_t)g.V * ESZ;  // past the row
+#pragma unroll 1
+            for (int j = 0; j <= NV; ++j) {
+                if (j == NV && (AL || lane)) break;
+                const unsigned char* q = p + j * 512;
+                if (q < stop) {
+                    const int bytes = (int)min((long long)16, (long long)(end - q));
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + j * 512), "l"(q), "r"(bytes) : "memory");
+                } else {
+                    slots[slot * kBeamSlot + j * 32 + lane] = make_uint4(ninf, ninf, ninf, ninf);
+                }
+            }
+        }
     };
-    float khi = 1.f, klo = 0.f;
-    uint4 v[NV];
-    load(row, batch, v);  // before it is known whether the row counts: one batch at most is read in vain
-    bool live = look(row);
-    beam_k(T, &khi, &klo);
+    float T, Tn = 0.f, Tk = -1.f, khi = 1.f, klo = 0.f;
+    int slot = 0;
+    copy(row, batch, 0);  // before it is known whether the row counts
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    bool live = look(row, T), liven = false;
     while (true) {
-        // the next batch of this row is on its way while this one is worked on
-        uint4 w[NV];
-        const bool more = left > 1 && batch + 1 < g.nb;
-        if (live && more) load(row, batch + 1, w);
+        // the next batch
+        const bool turn = batch + 1 == g.nb;
+        if (left > 1) {
+            if (turn) {
+                copy(row + 1, 0, slot ^ 1);
+                liven = look(row + 1, Tn);
+            } else if (live) {
+                copy(row, batch + 1, slot ^ 1);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
         if (live) {
-            float m[NV], mx;
+            if (T != Tk) {
+                beam_k(T, &khi, &klo);
+                Tk = T;
+            }
+            const uint4* at = slots + slot * kBeamSlot + lane;
+            uint4 v[NV];
+            if (AL) {
+#pragma unroll
+                for (int j = 0; j < NV; ++j) v[j] = at[j * 32];
+            } else {
+                __syncwarp();  // the other lanes' copies
+                const unsigned sh = (unsigned)(reinterpret_cast<uintptr_t>(base + (size_t)row * g.V * ESZ) & 15u);
+#pragma unroll
+                for (int j = 0; j < NV; ++j) v[j] = beam_shift(at[j * 32], at[j * 32 + 1], sh);
+                if ((batch + 1) * STEP > g.V) {  // elements past the row
+#pragma unroll
+                    for (int j = 0; j < NV; ++j) {
+                        const int n = (g.V - (batch * STEP + (j * 32 + lane) * VEC)) * ESZ;  // bytes of it
+                        uint32_t x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (4 * k >= n) x[k] = ninf;
+                            else if (ESZ == 2 && 4 * k + 2 >= n) x[k] = (x[k] & 0xffffu) | 0xff800000u;
+                        }
+                        v[j] = make_uint4(x[0], x[1], x[2], x[3]);
+                    }
+                }
+            }
+            float m[NV], mx = -INFINITY;
 #pragma unroll
             for (int j = 0; j < NV; ++j) m[j] = vec_max<ESZ>(v[j]);
+            float* cmax = g.cmax + ((size_t)row * g.nb + batch) * (NV * cpv);
             if (L == 32) {
+                float mine = 0.f;
 #pragma unroll
-                for (int j = 0; j < NV; ++j) m[j] = beam_warp_max(m[j]);
-                mx = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-                if (lane < NV) {
-                    const float x = lane == 0 ? m[0] : (lane == 1 ? m[1] : (lane == 2 ? m[2] : m[3]));
-                    g.cmax[((size_t)row * g.nb + batch) * NV + lane] = x;
+                for (int j = 0; j < NV; ++j) {
+                    m[j] = beam_warp_max(m[j]);
+                    mx = fmaxf(mx, m[j]);
+                    mine = lane == j ? m[j] : mine;
                 }
+                if (lane < NV) cmax[lane] = mine;
             } else {
                 for (int o = 1; o < L; o <<= 1)
 #pragma unroll
                     for (int j = 0; j < NV; ++j) m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], o));
-                if ((lane & (L - 1)) == 0)
 #pragma unroll
-                    for (int j = 0; j < NV; ++j)
-                        g.cmax[(((size_t)row * g.nb + batch) * NV + j) * cpv + (lane >> g.Lsh)] = m[j];
-                mx = beam_warp_max(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
+                for (int j = 0; j < NV; ++j) {
+                    if ((lane & (L - 1)) == 0) cmax[j * cpv + (lane >> g.Lsh)] = m[j];
+                    mx = fmaxf(mx, m[j]);
+                }
+                mx = beam_warp_max(mx);
             }
             unsigned long long acc[4];
 #pragma unroll
@@ -221,16 +297,14 @@ __global__ void __launch_bounds__(kBeamThreads, 4) sv_beam_rows(BeamArgs g, int 
             if (lane == 0) g.part[(size_t)row * g.nb + batch] = make_float2(mx, s);
         }
         if (--left <= 0) return;
-        if (++batch == g.nb) {
+        slot ^= 1;
+        if (turn) {
             batch = 0;
             ++row;
-            const float before = T;
-            load(row, 0, v);
-            live = look(row);
-            if (T != before) beam_k(T, &khi, &klo);
+            live = liven;
+            T = Tn;
         } else {
-#pragma unroll
-            for (int j = 0; j < NV; ++j) v[j] = w[j];
+            ++batch;
         }
     }
 }
@@ -257,16 +331,19 @@ __device__ __forceinline__ void pick_one_by_one(int want, unsigned long long* s_
     }
 }
 
-// How many of s_cand[0, n) rank before key; s_cand is 16-byte aligned and holds zeros
-// from n to the next multiple of 4.
-__device__ __forceinline__ int pick_rank(const unsigned long long* s_cand, int n, unsigned long long key)
+// How many of s_key[0, n) rank before number `me`: larger, or equal and earlier.  n is
+// taken up to a multiple of 4; s_key is 16-byte aligned and holds zeros from n on.
+__device__ __forceinline__ int pick_rank(const unsigned long long* s_key, int n, unsigned long long key, int me)
 {
     int rank = 0;
 #pragma unroll 2
     for (int o = 0; o < n; o += 4) {
-        const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(s_cand + o);
-        const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(s_cand + o + 2);
-        rank += (a.x > key) + (a.y > key) + (c.x > key) + (c.y > key);
+        const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(s_key + o);
+        const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(s_key + o + 2);
+        rank += a.x > key || (a.x == key && o < me);
+        rank += a.y > key || (a.y == key && o + 1 < me);
+        rank += c.x > key || (c.x == key && o + 2 < me);
+        rank += c.y > key || (c.y == key && o + 3 < me);
     }
     return rank;
 }
@@ -279,8 +356,10 @@ __global__ void __launch_bounds__(kPickThreads) sv_beam_pick(BeamArgs g)
     __shared__ double s_sum[kPickWarps], s_lse;
     __shared__ float s_top[kPickWarps];
     __shared__ __align__(16) unsigned long long s_cand[kBeamCap + 4];
+    __shared__ __align__(16) unsigned long long s_best[kPickThreads];
     __shared__ unsigned long long s_tmp[kPickWarps];
-    __shared__ int s_sel[SV_MAX_BEAMS];
+    __shared__ int s_at[kPickThreads];
+    __shared__ int s_sel[kPickChunks];
     __shared__ float s_tau, s_low;
     __shared__ int s_n, s_m, s_last;
     const int row = blockIdx.x, b = row / g.W, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -291,7 +370,7 @@ __global__ void __launch_bounds__(kPickThreads) sv_beam_pick(BeamArgs g)
     beam_k(t_ok ? T : 0.f, &khi, &klo);
     double* key = g.key + (size_t)row * g.K;
     int32_t* tok = g.tok + (size_t)row * g.K;
-    if (tid == 0) { s_n = 0; s_m = 0; s_low = -INFINITY; }
+    if (tid == 0) { s_n = 0; s_m = 0; }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     int cnt = 0, bad = 0;
     if (!(sc < INFINITY)) {
@@ -325,7 +404,7 @@ __global__ void __launch_bounds__(kPickThreads) sv_beam_pick(BeamArgs g)
             const float x0 = s_group[lane], x1 = s_group[32 + lane];
             const float mine = warp < 2 ? x0 : x1;
             const int first = warp * (GROUPS / kPickWarps);
-#pragma unroll
+#pragma unroll 4
             for (int q = 0; q < GROUPS / kPickWarps; ++q) {
                 const int me = first + q;
                 const float y = __shfl_sync(0xffffffffu, mine, me & 31);
@@ -353,7 +432,9 @@ __global__ void __launch_bounds__(kPickThreads) sv_beam_pick(BeamArgs g)
         if (!(top > -INFINITY && top < INFINITY) || S != S || (T > 0.f && !(S > 0.0 && S <= DBL_MAX && MK <= FLT_MAX))) {
             bad = SV_ROW_BAD_LOGITS;
         } else {
-            // ---- the `want` best chunks (and, meanwhile, the normaliser's logarithm)
+            // ---- the chunks that hold the `want` best logits: those at or above the bound, a
+            // few more than `want`; where ties make them many, exactly the `want` best
+            // (and, meanwhile, the normaliser's logarithm)
             const float tau = s_tau;
             if (tid == kPickThreads - 1) s_lse = ((double)MK + log2(S)) * kLn2;
             if (best >= tau) {
@@ -361,24 +442,15 @@ __global__ void __launch_bounds__(kPickThreads) sv_beam_pick(BeamArgs g)
                     const float x = cmax[c];
                     if (x >= tau && x > -INFINITY) {
                         const int at = atomicAdd(&s_n, 1);
-                        if (at < kBeamCap) s_cand[at] = beam_key(x, c);
+                        if (at < kPickChunks) s_sel[at] = c;
                     }
                 }
             }
             __syncthreads();
             int n = s_n;
-            if (n <= kBeamCap) {
-                if (tid < 4) s_cand[n + tid] = 0ull;
-                __syncthreads();
-                for (int c = tid; c < n; c += kPickThreads) {
-                    const unsigned long long k1 = s_cand[c];
-                    const int rank = pick_rank(s_cand, n, k1);
-                    if (rank < want) s_sel[rank] = (int)(0xffffffffu - (unsigned)k1);
-                    // every logit wanted is at or above the last chosen chunk's maximum (all
-                    // are wanted where the chunks are fewer)
-                    if (rank == want - 1) s_low = beam_unord((unsigned)(k1 >> 32));
-                }
-            } else {  // many equal maxima
+            float low = tau;  // every logit wanted is at or above it
+            if (n > kPickChunks) {
+                n = want;
                 pick_one_by_one(want, s_tmp,
                                 [&](auto f) {
                                     for (int c = tid; c < nch; c += kPickThreads) f(beam_key(cmax[c], c));
@@ -387,14 +459,14 @@ __global__ void __launch_bounds__(kPickThreads) sv_beam_pick(BeamArgs g)
                                     s_sel[k] = (int)(0xffffffffu - (unsigned)k1);
                                     s_low = beam_unord((unsigned)(k1 >> 32));
                                 });
+                __syncthreads();
+                low = s_low;
             }
-            __syncthreads();
             // ---- the logits of the chosen chunks
-            const float low = s_low;
             const unsigned char* base = static_cast<const unsigned char*>(g.logits);
             const unsigned char* end = base + (size_t)g.B * g.W * g.V * ESZ;
             const unsigned char* rp = base + (size_t)row * g.V * ESZ;
-            const int vectors = min(n, want) << g.Lsh;
+            const int vectors = n << g.Lsh;
             // first token of vector t of the chosen
             auto index = [&](int t) { return t < vectors ? s_sel[t >> g.Lsh] * CH + (t & (L - 1)) * VEC : g.V; };
             for (int t0 = tid; t0 < vectors; t0 += kPickThreads * NU) {
@@ -436,7 +508,7 @@ __global__ void __launch_bounds__(kPickThreads) sv_beam_pick(BeamArgs g)
                 __syncthreads();
                 for (int c = tid; c < n; c += kPickThreads) {
                     const unsigned long long k1 = s_cand[c];
-                    const int rank = pick_rank(s_cand, n, k1);
+                    const int rank = pick_rank(s_cand, n, k1, c);
                     if (rank < want) put(rank, k1);
                 }
             } else {  // many equal logits
@@ -467,48 +539,76 @@ __global__ void __launch_bounds__(kPickThreads) sv_beam_pick(BeamArgs g)
         __syncthreads();  // this row is the sequence
     }
     const size_t row0 = (size_t)b * g.W;
-    // the keys, as integers of their order, where the candidates' memory is no longer needed
-    const double* keys = g.key + row0 * g.K;
-    const bool fits = g.W * g.K <= kBeamCap;
-    auto ordered = [](double x) {
-        const unsigned long long u = (unsigned long long)__double_as_longlong(x + 0.0);
-        return u ^ ((u >> 63) ? ~0ull : 0x8000000000000000ull);
-    };
-    if (fits)
-        for (int c = tid; c < g.W * g.K; c += kPickThreads) s_cand[c] = ordered(__ldcg(keys + c));
+    // the keys, as integers of their order (0: none), where the candidates' memory is no
+    // longer needed; candidate c = w K + k, so ties go to the smaller c
+    const int all = g.W * g.K;
+    int* s_cnt = s_sel;
+    const int2 info = tid < g.W ? __ldcg(g.row_info + row0 + tid) : make_int2(0, 0);
+    if (tid < g.W) s_cnt[tid] = info.x;
+    if (warp == 0) {
+        const unsigned st = __reduce_or_sync(0xffffffffu, (unsigned)info.y);
+        if (g.out_status && lane == 0) g.out_status[b] = (int)(st | (t_ok ? 0u : SV_ROW_BAD_TEMPERATURE));
+    }
+    if (tid < 4) s_cand[all + tid] = 0ull;
     __syncthreads();
-    if (warp != 0) return;
-    // a lane per beam, its list's head in hand (0: none): the K largest heads one by one,
-    // ties to the lower beam
-    const int2 info = lane < g.W ? __ldcg(g.row_info + row0 + lane) : make_int2(0, 0);
-    const unsigned st = __reduce_or_sync(0xffffffffu, (unsigned)info.y);
-    if (g.out_status && lane == 0) g.out_status[b] = (int)(st | (t_ok ? 0u : SV_ROW_BAD_TEMPERATURE));
-    auto head = [&](int p) {
-        if (p >= info.x) return 0ull;
-        return fits ? s_cand[lane * g.K + p] : ordered(__ldcg(keys + lane * g.K + p));
-    };
-    int p = 0, parent = -1, place = 0;  // lane k: the k-th winner
-    unsigned long long now = head(0), after = head(1);
-    for (int k = 0; k < g.K; ++k) {
-        const unsigned long long top = beam_warp_max64(now);
-        if (top == 0ull) break;
-        const int who = __ffs(__ballot_sync(0xffffffffu, now == top)) - 1;
-        const int at = __shfl_sync(0xffffffffu, p, who);
-        if (lane == k) {
-            parent = who;
-            place = at;
+    unsigned long long best = 0ull;
+    for (int c = tid; c < all; c += kPickThreads) {
+        const int w = c / g.K;
+        unsigned long long o = 0ull;
+        if (c - w * g.K < s_cnt[w]) {
+            const unsigned long long u = (unsigned long long)__double_as_longlong(__ldcg(g.key + row0 * g.K + c) + 0.0);
+            o = u ^ ((u >> 63) ? ~0ull : 0x8000000000000000ull);
         }
-        if (lane == who) {
-            ++p;
-            now = after;
-            after = head(p + 1);
+        s_cand[c] = o;
+        best = max(best, o);
+    }
+    auto put = [&](int c, unsigned long long mine, int place) {
+        if (place >= g.K) return;
+        const size_t at = (size_t)b * g.K + place;
+        g.out_parent[at] = c / g.K;
+        g.out_token[at] = __ldcg(g.tok + row0 * g.K + c);
+        g.out_score[at] = (float)__longlong_as_double((long long)(mine ^ ((mine >> 63) ? 0x8000000000000000ull : ~0ull)));
+    };
+    bool rank_all = all <= kPickThreads;
+    if (!rank_all) {
+        // many candidates: only those at or above the K-th of the threads' largest matter
+        s_best[tid] = best;
+        if (tid == 0) s_n = 0;
+        __syncthreads();
+        if (pick_rank(s_best, kPickThreads, best, tid) == g.K - 1) s_tmp[0] = best;
+        __syncthreads();
+        const unsigned long long floor = max(1ull, s_tmp[0]);
+        for (int c = tid; c < all; c += kPickThreads)
+            if (s_cand[c] >= floor) {
+                const int at = atomicAdd(&s_n, 1);
+                if (at < kPickThreads) {
+                    s_best[at] = s_cand[c];
+                    s_at[at] = c;
+                }
+            }
+        __syncthreads();
+        const int n = s_n;
+        rank_all = n > kPickThreads;  // (many equal keys)
+        if (tid < n && !rank_all) {
+            const unsigned long long mine = s_best[tid];
+            const int c = s_at[tid];
+            int place = 0;
+#pragma unroll 4
+            for (int o = 0; o < n; ++o) place += s_best[o] > mine || (s_best[o] == mine && s_at[o] < c);
+            put(c, mine, place);
         }
     }
-    if (lane < g.K) {
-        const size_t at = (size_t)b * g.K + lane;
-        g.out_parent[at] = parent;
-        g.out_token[at] = parent < 0 ? -1 : __ldcg(g.tok + (row0 + parent) * g.K + place);
-        g.out_score[at] = parent < 0 ? -INFINITY : (float)__ldcg(keys + parent * g.K + place);
+    __syncthreads();
+    if (rank_all)
+        for (int c = tid; c < all; c += kPickThreads)
+            if (s_cand[c]) put(c, s_cand[c], pick_rank(s_cand, all, s_cand[c], c));
+    int total = 0;
+    for (int w = 0; w < g.W; ++w) total += s_cnt[w];
+    if (tid >= total && tid < g.K) {
+        const size_t at = (size_t)b * g.K + tid;
+        g.out_parent[at] = -1;
+        g.out_token[at] = -1;
+        g.out_score[at] = -INFINITY;
     }
 }
 
