@@ -7,7 +7,9 @@ tensors are not on a CUDA device, the call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 from typing import Dict, Tuple
 
@@ -523,36 +525,28 @@ def _check_q8(t: torch.Tensor, name: str, rows: int, K: int, device) -> int:
     return ld
 
 
-class _On:
-    """The device of the tensors and the stream of the call: what is allocated inside
-    belongs to that stream, so that its memory is not given away under a running kernel."""
-
-    __slots__ = ("device", "stream", "ctx")
-
-    def __init__(self, device, stream):
-        self.device, self.stream, self.ctx = device, stream, None
-
-    def __enter__(self):
-        if self.stream is not None:
-            self.ctx = torch.cuda.stream(self.stream)
-            self.ctx.__enter__()
-        elif torch.cuda.current_device() != self.device.index:
-            self.ctx = torch.cuda.device(self.device)
-            self.ctx.__enter__()
-        if self.stream is not None and self.stream.device != self.device:
-            self.__exit__(None, None, None)
-            raise ValueError(f"the stream must be on {self.device}, got {self.stream.device}")
-        return (self.stream if self.stream is not None else torch.cuda.current_stream(self.device)).cuda_stream
-
-    def __exit__(self, *a):
-        if self.ctx is not None:
-            self.ctx.__exit__(*a)
-            self.ctx = None
+@contextlib.contextmanager
+def _on_stream(device, stream):
+    with torch.cuda.device(device) if stream is None else torch.cuda.stream(stream):
+        yield torch.cuda.current_stream(device).cuda_stream
 
 
-def _q8_empty(rows: int, K: int, device):
-    q = torch.empty((rows, _q8_stride(K)), dtype=torch.int8, device=device)
-    return q[:, :K], torch.empty((rows,), dtype=torch.float32, device=device)
+def _on(device: torch.device, stream: torch.cuda.Stream | None):
+    """A context with the tensors' device and the call's stream current (its value: the
+    stream's handle).  What is allocated inside belongs to that stream, so its memory is
+    not given away under a running kernel."""
+    if stream is None and torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext(torch._C._cuda_getCurrentRawStream(device.index))  # the common case, cheaply
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream must be on {device}, got {stream.device}")
+    return _on_stream(device, stream)
+
+
+def _q8_empty(like: torch.Tensor, rows: int, K: int):
+    """Int8 rows at a pitch that is a multiple of 16 bytes, and their scales."""
+    ld = _q8_stride(K)
+    q = torch.empty_strided((rows, K), (ld, 1), dtype=torch.int8, device=like.device)
+    return q, like.new_empty((rows,), dtype=torch.float32), ld
 
 
 def q8_quantize(x: torch.Tensor, *, stream: torch.cuda.Stream | None = None):
@@ -564,9 +558,9 @@ def q8_quantize(x: torch.Tensor, *, stream: torch.cuda.Stream | None = None):
     M, K = x.shape
     dt = _dt_code(x.dtype)
     _check(x, "x", None, (M, K), device)
-    with _On(device, stream) as s:
-        q, scale = _q8_empty(M, K, device)
-        _raise_if(lib.spec_verify_q8_quantize(x.data_ptr(), dt, M, K, q.data_ptr(), _q8_stride(K), scale.data_ptr(), s))
+    with _on(device, stream) as s:
+        q, scale, ld = _q8_empty(x, M, K)
+        _raise_if(lib.spec_verify_q8_quantize(x.data_ptr(), dt, M, K, q.data_ptr(), ld, scale.data_ptr(), s))
     return q, scale
 
 
@@ -585,13 +579,13 @@ def q8_norm(x: torch.Tensor, weight: torch.Tensor | None, eps: float, *, residua
         _check(weight, "weight", x.dtype, (d,), device)
     if residual is not None:
         _check(residual, "residual", x.dtype, (M, d), device)
-    with _On(device, stream) as s:
-        q, scale = _q8_empty(M, d, device)
+    with _on(device, stream) as s:
+        q, scale, ld = _q8_empty(x, M, d)
         total = torch.empty_like(x) if residual is not None else None
         normed = torch.empty_like(x) if with_normed else None
         _raise_if(lib.spec_verify_q8_norm(x.data_ptr(), residual.data_ptr() if residual is not None else None,
                                           weight.data_ptr() if weight is not None else None, dt, eps, M, d,
-                                          q.data_ptr(), _q8_stride(d), scale.data_ptr(),
+                                          q.data_ptr(), ld, scale.data_ptr(),
                                           total.data_ptr() if total is not None else None,
                                           normed.data_ptr() if normed is not None else None, s))
     out = (q, scale)
@@ -619,8 +613,8 @@ def q8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: 
     if error is not None:
         _check(error, "error", torch.int32, (1,), device)
     dt = _dt_code(dtype)
-    with _On(device, stream) as s:
-        z = torch.empty((M, V), dtype=dtype, device=device)
+    with _on(device, stream) as s:
+        z = a.new_empty((M, V), dtype=dtype)
         _raise_if(lib.spec_verify_q8_matmul(a.data_ptr(), lda, a_scale.data_ptr(), w.data_ptr(), ldw, w_scale.data_ptr(),
                                             M, K, V, z.data_ptr(), dt, error.data_ptr() if error is not None else None, s))
     return z
@@ -648,7 +642,7 @@ def q8_head(x: torch.Tensor, weight: torch.Tensor | None, eps: float, w: torch.T
         _check(error, "error", torch.int32, (1,), device)
     if workspace is not None:
         _check(workspace, "workspace", torch.uint8, (workspace.numel(),), device)
-    with _On(device, stream) as s:
+    with _on(device, stream) as s:
         if workspace is None:
             workspace = torch.empty(lib.spec_verify_q8_head_workspace_size(M, d), dtype=torch.uint8, device=device)
         z = torch.empty((M, V), dtype=dtype, device=device)
@@ -659,6 +653,11 @@ def q8_head(x: torch.Tensor, weight: torch.Tensor | None, eps: float, w: torch.T
                                           z.data_ptr(), dt, workspace.data_ptr(), workspace.numel(),
                                           error.data_ptr() if error is not None else None, s))
     return z if total is None else (z, total)
+
+
+@functools.lru_cache(maxsize=256)
+def _beam_workspace(B: int, W: int, V: int, K: int, dt: int) -> int:
+    return load_library().spec_verify_beam_workspace_size(B, W, V, K, dt)
 
 
 def beam_select(logits: torch.Tensor, scores: torch.Tensor, temperature: torch.Tensor, K: int, *,
@@ -681,17 +680,17 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, temperature: torch.T
         _check(frozen, "frozen", torch.int32, (B, W), device)
     if workspace is not None:
         _check(workspace, "workspace", torch.uint8, (workspace.numel(),), device)
-    need = lib.spec_verify_beam_workspace_size(B, W, V, K, dt)
+    need = _beam_workspace(B, W, V, K, dt)
     if need == 0:
         raise SpecVerifyError(1, f"beam_select takes W and K in [1, {MAX_BEAMS}], V in [1, {1 << 20}] and B >= 1; got "
                                  f"B={B}, W={W}, V={V}, K={K}")
-    with _On(device, stream) as s:
+    with _on(device, stream) as s:
         if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        parent = torch.empty((B, K), dtype=torch.int32, device=device)
-        token = torch.empty((B, K), dtype=torch.int32, device=device)
-        score = torch.empty((B, K), dtype=torch.float32, device=device)
-        status = torch.empty((B,), dtype=torch.int32, device=device) if return_row_status else None
+            workspace = logits.new_empty((need,), dtype=torch.uint8)
+        parent = scores.new_empty((B, K), dtype=torch.int32)
+        token = scores.new_empty((B, K), dtype=torch.int32)
+        score = scores.new_empty((B, K))
+        status = scores.new_empty((B,), dtype=torch.int32) if return_row_status else None
         _raise_if(lib.spec_verify_beam_select(logits.data_ptr(), dt, scores.data_ptr(), temperature.data_ptr(),
                                               frozen.data_ptr() if frozen is not None else None, int(pad_token), B, W, V,
                                               K, parent.data_ptr(), token.data_ptr(), score.data_ptr(),
@@ -720,7 +719,7 @@ def beam_reorder(src: torch.Tensor, parent: torch.Tensor, *, out: torch.Tensor |
         _check(lengths, "lengths", torch.int32, (B,), device)
     if out is not None:
         _check(out, "out", src.dtype, (L, B, K, H, S, D), device)
-    with _On(device, stream) as s:
+    with _on(device, stream) as s:
         if out is None:
             out = torch.zeros((L, B, K, H, S, D), dtype=src.dtype, device=device)
         _raise_if(lib.spec_verify_beam_reorder(src.data_ptr(), out.data_ptr(), parent.data_ptr(),
