@@ -7,6 +7,8 @@
 #include <cuda.h>  // CUtensorMap: driver calls go through entry points
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <stdlib.h>
+#include <stdio.h>
 
 #include <algorithm>
 #include <atomic>
@@ -124,27 +126,70 @@ bool q8_map(CUtensorMap* m, const void* base, long long rows, long long K, long 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Whether the product runs on pairs of SMs.
+bool q8_pairs(const Q8GemmArgs& g)
+{
+    static const char* force = getenv("Q8P");
+    if (force) return force[0] == '1';
+    return g.M > 64;
+}
+
 template <int ESZ>
 cudaError_t q8_gemm_launch(const void* a, long long lda, const void* w, long long ldw, Q8GemmArgs g, cudaStream_t st)
 {
+    const int sms = device_sm_count();
+    const bool pairs = q8_pairs(g);
     // as few token tiles as 256 tokens each allow, all of one size
+    const int unit = pairs ? 32 : 16;
     g.m_tiles = (int)cdiv(g.M, kQ8MaxNT);
-    g.nt = (int)(cdiv(cdiv(g.M, g.m_tiles), 16) * 16);
+    g.nt = (int)(cdiv(cdiv(g.M, g.m_tiles), unit) * unit);
     g.m_tiles = (int)cdiv(g.M, g.nt);
-    g.v_tiles = (int)cdiv(g.V, kQ8BM);
+    g.v_tiles = (int)cdiv(g.V, pairs ? 2 * kQ8BM : kQ8BM);
     g.tmem_cols = 32;
     while (g.tmem_cols < 2 * g.nt) g.tmem_cols *= 2;
-    const int stage = kQ8WBytes + g.nt * kQ8BK;
+    const int mine = pairs ? g.nt / 2 : g.nt;  // tokens of a stage in one CTA
+    const int stage = kQ8WBytes + mine * kQ8BK;
     g.stages = std::min(kQ8MaxStages, (kQ8SmemMax - 1024) / stage);
     CUtensorMap tw, ta;
-    if (!q8_map(&tw, w, g.V, g.K, ldw, kQ8BM) || !q8_map(&ta, a, g.M, g.K, lda, g.nt)) return cudaErrorInvalidValue;
-    static std::atomic<bool> ready[kMaxDevices];
-    const cudaError_t e = allow_smem(sv_q8_gemm<ESZ>, kQ8SmemMax, ready);
-    if (e != cudaSuccess) return e;
+    if (!q8_map(&tw, w, g.V, g.K, ldw, kQ8BM) || !q8_map(&ta, a, g.M, g.K, lda, mine)) return cudaErrorInvalidValue;
     const long long tiles = (long long)g.m_tiles * g.v_tiles;
-    const long long grid = std::min<long long>(tiles, device_sm_count());
-    sv_q8_gemm<ESZ><<<(unsigned)grid, kQ8Threads, 1024 + g.stages * stage, st>>>(tw, ta, g);
-    return cudaGetLastError();
+    const int smem = 1024 + g.stages * stage;
+    static std::atomic<bool> ready[kMaxDevices], ready2[kMaxDevices];
+    if (!pairs) {
+        const cudaError_t e = allow_smem(sv_q8_gemm<ESZ>, kQ8SmemMax, ready);
+        if (e != cudaSuccess) return e;
+        sv_q8_gemm<ESZ><<<(unsigned)std::min<long long>(tiles, sms), kQ8Threads, smem, st>>>(tw, ta, g);
+        return cudaGetLastError();
+    }
+    cudaError_t e = allow_smem(sv_q8_gemm_pair<ESZ>, kQ8SmemMax, ready2);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kQ8Threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    // as many pairs as are resident at once (an SM without a partner in its GPC has none)
+    static std::atomic<int> resident[kMaxDevices];
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    int n = dev >= 0 && dev < kMaxDevices ? resident[dev].load(std::memory_order_relaxed) : 0;
+    if (!n) {
+        cfg.gridDim = dim3((unsigned)(2 * (sms / 2)));
+        cfg.dynamicSmemBytes = kQ8SmemMax;
+        if ((e = cudaOccupancyMaxActiveClusters(&n, sv_q8_gemm_pair<ESZ>, &cfg)) != cudaSuccess) return e;
+        if (n < 1) return cudaErrorInvalidConfiguration;
+        cfg.dynamicSmemBytes = (size_t)smem;
+        if (getenv("Q8P")) printf("pairs resident %d\n", n);
+        if (dev >= 0 && dev < kMaxDevices) resident[dev].store(n, std::memory_order_relaxed);
+    }
+    cfg.gridDim = dim3((unsigned)(2 * std::min<long long>(tiles, n)));
+    return cudaLaunchKernelEx(&cfg, sv_q8_gemm_pair<ESZ>, tw, ta, g);
 }
 
 sv_status q8_gemm_check(const void* a, int lda, const void* a_scale, const void* w, int ldw, const void* w_scale, int M,

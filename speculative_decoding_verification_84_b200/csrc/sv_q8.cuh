@@ -524,6 +524,70 @@ __device__ __forceinline__ void q8_tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+// The producer and the MMA issuer are whole warps in step, one elected lane of which
+// issues: addresses, descriptors and loop counts then live in uniform registers, where
+// the copies and MMAs want them (from one thread's registers every issue moved its
+// operands first, and a stage took Q8_SERIAL cycles whatever its products).
+__device__ __forceinline__ bool q8_elect()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// lr_wait by a warp, one answer for all lanes
+__device__ __forceinline__ bool q8_wait(uint64_t* bar, unsigned parity, volatile int* abort, int* err)
+{
+    return __all_sync(0xffffffffu, lr_wait(bar, parity, abort, err)) != 0;
+}
+
+// A place in the ring of stages and its phase: counted, not divided for.
+struct Q8Ring {
+    int s = 0;
+    unsigned phase = 0;
+    __device__ __forceinline__ void next(int S)
+    {
+        if (++s == S) {
+            s = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+// The logits of channel v (one a lane) and the tile's tokens, from the accumulator at
+// acc: 16-column chunks grp, grp + 2, ...  A bf16 row of even length goes out in words:
+// two lanes trade a value, so each stores a channel pair of one of two tokens.
+template <int ESZ>
+__device__ __forceinline__ void q8_epilogue(const Q8GemmArgs& g, uint32_t acc, int grp, int m0, int v)
+{
+    const float sw = v < g.V ? __ldg(g.w_scale + v) : 0.f;
+    const bool words = ESZ == 2 && (g.V & 1) == 0;
+    const int odd = v & 1;
+    for (int c = grp * 16; c < g.nt && m0 + c < g.M; c += 32) {
+        uint32_t r[16];
+        q8_tmem_ld16(acc + (uint32_t)c, r);
+        float z[16];
+        const int left = g.M - (m0 + c);  // tokens from here on
+#pragma unroll
+        for (int j = 0; j < 16; ++j) z[j] = (float)(int)r[j] * ((j < left ? __ldg(g.a_scale + m0 + c + j) : 0.f) * sw);
+        if (words) {
+            uint32_t* to = static_cast<uint32_t*>(g.out) + ((size_t)(m0 + c + odd) * g.V + (v - odd)) / 2;
+            const size_t step = (size_t)g.V;  // words of two rows
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+                const float other = __shfl_xor_sync(0xffffffffu, odd ? z[j] : z[j + 1], 1);
+                const __nv_bfloat162 h = odd ? __floats2bfloat162_rn(other, z[j + 1]) : __floats2bfloat162_rn(z[j], other);
+                if (j + odd < left && v < g.V) *to = *reinterpret_cast<const uint32_t*>(&h);
+                to += step;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (j < left && v < g.V) q8_st1<ESZ>(g.out, (size_t)(m0 + c + j) * g.V + v, z[j]);
+        }
+    }
+}
+
 // Persistent, one CTA per SM; tiles blockIdx.x, blockIdx.x + gridDim.x, ... with
 // the token tile fastest, so the CTAs that share weights run at about the same time.
 // Every wait on an mbarrier is bounded: past kLrPolls polls the CTA raises *err,
@@ -569,45 +633,55 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     volatile int* abort = &s_abort;
 
     int issued = 0;
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         // ---- producer: one global count of stages across the CTA's tiles
-        int it = 0;
+        Q8Ring r;
         bool ok = true;
         for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
             const int m0 = (int)(t % g.m_tiles) * g.nt, v0 = (int)(t / g.m_tiles) * kQ8BM;
-            for (int kb = 0; kb < kbs; ++kb, ++it) {
-                const int s = it % S;
-                if (it >= S && !lr_wait(&empty[s], (unsigned)(it / S - 1) & 1u, abort, g.err)) { ok = false; break; }
-                unsigned char* st = ring + s * STAGE;
-                lr_expect_tx(&full[s], (unsigned)STAGE);
-                lr_tma_2d(st, &tw, &full[s], kb * kQ8BK, v0);
-                lr_tma_2d(st + kQ8WBytes, &ta, &full[s], kb * kQ8BK, m0);
-                issued = it + 1;
+            for (int kb = 0; kb < kbs; ++kb) {
+                if (issued >= S && !q8_wait(&empty[r.s], r.phase ^ 1u, abort, g.err)) { ok = false; break; }
+                if (q8_elect()) {
+                    unsigned char* st = ring + r.s * STAGE;
+                    lr_expect_tx(&full[r.s], (unsigned)STAGE);
+                    lr_tma_2d(st, &tw, &full[r.s], kb * kQ8BK, v0);
+                    lr_tma_2d(st + kQ8WBytes, &ta, &full[r.s], kb * kQ8BK, m0);
+                }
+                __syncwarp();
+                ++issued;
+                r.next(S);
             }
         }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
         // ---- MMA issuer
         const uint32_t idesc = q8_idesc(g.nt);
-        int it = 0, i = 0;
+        const uint64_t wd0 = lr_desc(lr_smem(ring)), ad0 = lr_desc(lr_smem(ring) + kQ8WBytes);
+        Q8Ring r;
+        int consumed = 0, i = 0;
         bool ok = true;
         for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++i) {
             const int b = i & 1, use = i >> 1;
-            if (use >= 1 && !lr_wait(&tempty[b], (unsigned)(use - 1) & 1u, abort, g.err)) break;
+            if (use >= 1 && !q8_wait(&tempty[b], (unsigned)(use - 1) & 1u, abort, g.err)) break;
             lr_fence_after();
             const uint32_t d = tmem + (uint32_t)(b * (g.tmem_cols / 2));
-            for (int kb = 0; kb < kbs; ++kb, ++it) {
-                const int s = it % S;
-                if (!lr_wait(&full[s], (unsigned)(it / S) & 1u, abort, g.err)) { ok = false; break; }
+            for (int kb = 0; kb < kbs; ++kb) {
+                if (!q8_wait(&full[r.s], r.phase, abort, g.err)) { ok = false; break; }
                 lr_fence_after();
-                const uint32_t w0 = lr_smem(ring + s * STAGE), a0 = w0 + kQ8WBytes;
+                if (q8_elect()) {
+                    const uint64_t off = (uint64_t)((unsigned)(r.s * STAGE) >> 4);
 #pragma unroll
-                for (int j = 0; j < kQ8BK / 32; ++j)  // K = 32 per MMA: 32 bytes along the swizzled row
-                    q8_mma(d, lr_desc(w0 + 32 * j), lr_desc(a0 + 32 * j), idesc, (kb > 0 || j > 0) ? 1u : 0u);
-                lr_commit(&empty[s]);
-                s_consumed = it + 1;
+                    for (int j = 0; j < kQ8BK / 32; ++j)  // K = 32 per MMA: 32 bytes along the swizzled row
+                        q8_mma(d, wd0 + off + 2 * j, ad0 + off + 2 * j, idesc, (kb > 0 || j > 0) ? 1u : 0u);
+                    lr_commit(&empty[r.s]);
+                }
+                __syncwarp();
+                ++consumed;
+                r.next(S);
             }
-            lr_commit(&tfull[b]);
+            if (ok && q8_elect()) lr_commit(&tfull[b]);
+            __syncwarp();
         }
+        if (lane == 0) s_consumed = consumed;
     } else if (warp >= 4) {
         // ---- epilogue: warp 4 + e owns TMEM lanes (= channels of the tile) 32q .. 32q + 31,
         // q = e % 4, and the 16-column chunks e / 4, e / 4 + 2, ...
@@ -617,7 +691,6 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
             const int b = i & 1, use = i >> 1;
             const int m0 = (int)(t % g.m_tiles) * g.nt;
             const int v = (int)(t / g.m_tiles) * kQ8BM + 32 * q + lane;
-            const float sw = v < g.V ? __ldg(g.w_scale + v) : 0.f;
             // one lane waits, so the warp-wide tcgen05.ld below runs on all lanes or none
             int ready = 0;
             if (lane == 0) ready = lr_wait(&tfull[b], (unsigned)use & 1u, abort, g.err) ? 1 : 0;
@@ -625,18 +698,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
             if (!ready) break;
             lr_fence_after();
             const uint32_t acc = tmem + (uint32_t)(b * (g.tmem_cols / 2)) + ((uint32_t)(32 * q) << 16);
-            for (int c = grp * 16; c < g.nt && m0 + c < g.M; c += 32) {
-                uint32_t r[16];
-                q8_tmem_ld16(acc + (uint32_t)c, r);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const int m = m0 + c + j;
-                    if (m < g.M && v < g.V) {
-                        const float z = (float)(int)r[j] * (__ldg(g.a_scale + m) * sw);
-                        q8_st1<ESZ>(g.out, (size_t)m * g.V + v, z);
-                    }
-                }
-            }
+            q8_epilogue<ESZ>(g, acc, grp, m0, v);
             lr_fence_before();
             __syncwarp();
             if (lane == 0) lr_arrive(&tempty[b]);
@@ -656,6 +718,194 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     if (warp == 2) {
         lr_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(g.tmem_cols));
+    }
+}
+
+// ---- pairs of CTAs (cta_group::2): one MMA of M = 256 over two SMs.  Each CTA holds its
+// 128 channels and HALF the tokens of the tile, and gets all of the tile's columns for its
+// channels, so an SM's shared memory is filled and read with two thirds of the bytes a
+// product (nt = 256: 8 KB read an MMA and 32 KB filled a stage, against 12 and 48).
+// rank 0 of the cluster waits, issues and commits for both.
+
+__device__ __forceinline__ uint32_t q8_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// the address of the leader's copy of a shared variable
+__device__ __forceinline__ uint32_t q8_leader(const void* p)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(lr_smem(p)));
+    return a;
+}
+
+// to this CTA's shared memory, counted by the leader's barrier
+__device__ __forceinline__ void q8_tma_pair(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+            lr_smem(dst)),
+        "l"((uint64_t)map), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+
+__device__ __forceinline__ void q8_mma_pair(uint32_t tmem_d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(da), "l"(db), "r"(idesc), "r"(accumulate));
+}
+
+// both CTAs' copies of a barrier, once this thread's MMAs are done
+__device__ __forceinline__ void q8_commit_pair(uint64_t* bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                     lr_smem(bar)),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
+
+__device__ __forceinline__ void q8_cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <int ESZ>
+__global__ void __launch_bounds__(kQ8Threads, 1)
+    sv_q8_gemm_pair(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap ta, Q8GemmArgs g)
+{
+    extern __shared__ unsigned char q8_dyn[];
+    // the same offset in both CTAs, every stage on a 1024-byte boundary of the shared window
+    unsigned char* ring = q8_dyn + ((1024u - (lr_smem(q8_dyn) & 1023u)) & 1023u);
+    __shared__ __align__(8) uint64_t full[kQ8MaxStages], empty[kQ8MaxStages], tfull[2], tempty[2];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)q8_rank();
+    const int kbs = (g.K + kQ8BK - 1) / kQ8BK, S = g.stages, half = g.nt / 2;
+    const int STAGE = kQ8WBytes + half * kQ8BK;
+    const long long tiles = (long long)g.m_tiles * g.v_tiles;  // v_tiles of 256 channels
+    const long long pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            lr_mbar_init(&full[s], 1);
+            lr_mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            lr_mbar_init(&tfull[b], 1);
+            lr_mbar_init(&tempty[b], 2 * kQ8EpiWarps);
+        }
+        s_abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(lr_smem(&s_tmem)),
+                     "r"(g.tmem_cols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
+    lr_fence_before();
+    __syncthreads();
+    q8_cluster_sync();  // both CTAs' barriers stand before either is reached from the other
+    lr_fence_after();
+    const uint32_t tmem = s_tmem;
+    volatile int* abort = &s_abort;
+
+    if (warp == 0) {
+        // ---- producer of this CTA's share of every stage
+        Q8Ring r;
+        int it = 0;
+        bool ok = true;
+        const uint32_t bars = q8_leader(full);
+        for (long long t = pair; ok && t < tiles; t += pairs) {
+            const int m0 = (int)(t % g.m_tiles) * g.nt + rank * half, v0 = (int)(t / g.m_tiles) * 2 * kQ8BM + rank * kQ8BM;
+            for (int kb = 0; kb < kbs; ++kb) {
+                if (it >= S && !q8_wait(&empty[r.s], r.phase ^ 1u, abort, g.err)) { ok = false; break; }
+                if (q8_elect()) {
+                    unsigned char* st = ring + r.s * STAGE;
+                    if (rank == 0) lr_expect_tx(&full[r.s], 2u * (unsigned)STAGE);
+                    q8_tma_pair(st, &tw, bars + 8u * r.s, kb * kQ8BK, v0);
+                    q8_tma_pair(st + kQ8WBytes, &ta, bars + 8u * r.s, kb * kQ8BK, m0);
+                }
+                __syncwarp();
+                ++it;
+                r.next(S);
+            }
+        }
+        // every stage handed back: nothing of the pair's is still on its way to this CTA
+        for (int u = max(0, it - S); ok && u < it; ++u) ok = q8_wait(&empty[u % S], (unsigned)(u / S) & 1u, abort, g.err);
+    } else if (warp == 1 && rank == 0) {
+        // ---- MMA issuer of the pair
+        const uint32_t idesc = (q8_idesc(g.nt) & ~(31u << 24)) | ((uint32_t)(2 * kQ8BM >> 4) << 24);
+        const uint64_t wd0 = lr_desc(lr_smem(ring)), ad0 = lr_desc(lr_smem(ring) + kQ8WBytes);
+        Q8Ring r;
+        int i = 0;
+        bool ok = true;
+        for (long long t = pair; ok && t < tiles; t += pairs, ++i) {
+            const int b = i & 1, use = i >> 1;
+            if (use >= 1 && !q8_wait(&tempty[b], (unsigned)(use - 1) & 1u, abort, g.err)) break;
+            lr_fence_after();
+            const uint32_t d = tmem + (uint32_t)(b * (g.tmem_cols / 2));
+            for (int kb = 0; kb < kbs; ++kb) {
+                if (!q8_wait(&full[r.s], r.phase, abort, g.err)) { ok = false; break; }
+                lr_fence_after();
+                if (q8_elect()) {
+                    const uint64_t off = (uint64_t)((unsigned)(r.s * STAGE) >> 4);
+#pragma unroll
+                    for (int j = 0; j < kQ8BK / 32; ++j)
+                        q8_mma_pair(d, wd0 + off + 2 * j, ad0 + off + 2 * j, idesc, (kb > 0 || j > 0) ? 1u : 0u);
+                    q8_commit_pair(&empty[r.s]);
+                }
+                __syncwarp();
+                r.next(S);
+            }
+            if (ok && q8_elect()) q8_commit_pair(&tfull[b]);
+            __syncwarp();
+        }
+    } else if (warp >= 4) {
+        // ---- epilogue of this CTA's 128 channels, as sv_q8_gemm's
+        const int q = (warp - 4) & 3, grp = (warp - 4) >> 2;
+        int i = 0;
+        for (long long t = pair; t < tiles; t += pairs, ++i) {
+            const int b = i & 1, use = i >> 1;
+            const int m0 = (int)(t % g.m_tiles) * g.nt;
+            const int v = (int)(t / g.m_tiles) * 2 * kQ8BM + rank * kQ8BM + 32 * q + lane;
+            int ready = 0;
+            if (lane == 0) ready = lr_wait(&tfull[b], (unsigned)use & 1u, abort, g.err) ? 1 : 0;
+            ready = __shfl_sync(0xffffffffu, ready, 0);
+            if (!ready) break;
+            lr_fence_after();
+            q8_epilogue<ESZ>(g, tmem + (uint32_t)(b * (g.tmem_cols / 2)) + ((uint32_t)(32 * q) << 16), grp, m0, v);
+            lr_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(q8_leader(&tempty[b])) : "memory");
+        }
+    }
+    // after a wait gave up: time for the copies in flight to land before the memory goes
+    // away (two milliseconds, a thousand times what one takes)
+    if (threadIdx.x == 0 && s_abort) {
+        uint64_t t0, t1;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+        for (unsigned k = 0; k < kLrPolls; ++k) {
+            asm volatile("nanosleep.u32 1000;");
+            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t1));
+            if (t1 - t0 > 2000000u) break;
+        }
+    }
+    lr_fence_before();
+    __syncthreads();
+    q8_cluster_sync();  // neither CTA leaves while the other may still reach its barriers
+    if (warp == 2) {
+        lr_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(g.tmem_cols));
     }
 }
 
