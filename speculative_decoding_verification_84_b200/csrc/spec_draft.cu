@@ -134,21 +134,32 @@ bool q8_pairs(const Q8GemmArgs& g)
     return g.M > 64;
 }
 
+int q8_groups(const Q8GemmArgs& g, long long accs)
+{
+    static const char* force = getenv("Q8G");
+    if (force) return accs > 1 ? force[0] - '0' : 1;
+    return accs == 2 ? 2 : 1;
+}
+
 template <int ESZ>
 cudaError_t q8_gemm_launch(const void* a, long long lda, const void* w, long long ldw, Q8GemmArgs g, cudaStream_t st)
 {
     const int sms = device_sm_count();
     const bool pairs = q8_pairs(g);
-    // as few token tiles as 256 tokens each allow, all of one size
+    // as few accumulators of 256 tokens as hold the batch, all of one size; two to a tile
+    // where that is the whole batch (the weights are then read once)
     const int unit = pairs ? 32 : 16;
-    g.m_tiles = (int)cdiv(g.M, kQ8MaxNT);
-    g.nt = (int)(cdiv(cdiv(g.M, g.m_tiles), unit) * unit);
-    g.m_tiles = (int)cdiv(g.M, g.nt);
+    const long long accs = cdiv(g.M, kQ8MaxNT);
+    g.nt = (int)(cdiv(cdiv(g.M, accs), unit) * unit);
+    g.groups = q8_groups(g, accs);
+    g.m_tiles = (int)cdiv(g.M, (long long)g.nt * g.groups);
     g.v_tiles = (int)cdiv(g.V, pairs ? 2 * kQ8BM : kQ8BM);
+    g.buf_cols = (int)(cdiv(g.nt, 32) * 32);
+    g.bufs = std::min(kQ8MaxBufs, 512 / g.buf_cols);
     g.tmem_cols = 32;
-    while (g.tmem_cols < 2 * g.nt) g.tmem_cols *= 2;
-    const int mine = pairs ? g.nt / 2 : g.nt;  // tokens of a stage in one CTA
-    const int stage = kQ8WBytes + mine * kQ8BK;
+    while (g.tmem_cols < g.bufs * g.buf_cols) g.tmem_cols *= 2;
+    const int mine = pairs ? g.nt / 2 : g.nt;  // tokens of an accumulator in one CTA
+    const int stage = kQ8Sub * (kQ8WBytes + g.groups * mine * kQ8BK);
     g.stages = std::min(kQ8MaxStages, (kQ8SmemMax - 1024) / stage);
     CUtensorMap tw, ta;
     if (!q8_map(&tw, w, g.V, g.K, ldw, kQ8BM) || !q8_map(&ta, a, g.M, g.K, lda, mine)) return cudaErrorInvalidValue;
@@ -156,12 +167,12 @@ cudaError_t q8_gemm_launch(const void* a, long long lda, const void* w, long lon
     const int smem = 1024 + g.stages * stage;
     static std::atomic<bool> ready[kMaxDevices], ready2[kMaxDevices];
     if (!pairs) {
-        const cudaError_t e = allow_smem(sv_q8_gemm<ESZ>, kQ8SmemMax, ready);
+        const cudaError_t e = allow_smem(sv_q8_gemm<ESZ, false>, kQ8SmemMax, ready);
         if (e != cudaSuccess) return e;
-        sv_q8_gemm<ESZ><<<(unsigned)std::min<long long>(tiles, sms), kQ8Threads, smem, st>>>(tw, ta, g);
+        sv_q8_gemm<ESZ, false><<<(unsigned)std::min<long long>(tiles, sms), kQ8Threads, smem, st>>>(tw, ta, g);
         return cudaGetLastError();
     }
-    cudaError_t e = allow_smem(sv_q8_gemm_pair<ESZ>, kQ8SmemMax, ready2);
+    cudaError_t e = allow_smem(sv_q8_gemm<ESZ, true>, kQ8SmemMax, ready2);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kQ8Threads);
@@ -182,14 +193,13 @@ cudaError_t q8_gemm_launch(const void* a, long long lda, const void* w, long lon
     if (!n) {
         cfg.gridDim = dim3((unsigned)(2 * (sms / 2)));
         cfg.dynamicSmemBytes = kQ8SmemMax;
-        if ((e = cudaOccupancyMaxActiveClusters(&n, sv_q8_gemm_pair<ESZ>, &cfg)) != cudaSuccess) return e;
+        if ((e = cudaOccupancyMaxActiveClusters(&n, sv_q8_gemm<ESZ, true>, &cfg)) != cudaSuccess) return e;
         if (n < 1) return cudaErrorInvalidConfiguration;
         cfg.dynamicSmemBytes = (size_t)smem;
-        if (getenv("Q8P")) printf("pairs resident %d\n", n);
         if (dev >= 0 && dev < kMaxDevices) resident[dev].store(n, std::memory_order_relaxed);
     }
     cfg.gridDim = dim3((unsigned)(2 * std::min<long long>(tiles, n)));
-    return cudaLaunchKernelEx(&cfg, sv_q8_gemm_pair<ESZ>, tw, ta, g);
+    return cudaLaunchKernelEx(&cfg, sv_q8_gemm<ESZ, true>, tw, ta, g);
 }
 
 sv_status q8_gemm_check(const void* a, int lda, const void* a_scale, const void* w, int ldw, const void* w_scale, int M,

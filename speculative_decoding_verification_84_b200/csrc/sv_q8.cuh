@@ -17,12 +17,11 @@
 // 128 * 128 * K both below 2^31).  The weights are the MMA's 128 rows and the
 // tokens its columns, so a small batch pads to 16 tokens, not to 128, and every
 // weight byte crosses to an SM once per token tile (up to 256 tokens).
-//   warp 0 (one thread)  TMA: 128 x 128 bytes of weights and nt x 128 of tokens per
-//                        stage, 128-byte swizzle, an mbarrier ring
-//   warp 1 (one thread)  tcgen05.mma, M = 128, N = nt, four K = 32 steps per stage
-//   warp 2               TMEM columns (two accumulators of nt columns)
-//   warps 4-11           epilogue: lane = channel, column = token; scales, rounding,
-//                        stores
+//   warp 0     TMA: per stage two K blocks of 128 x 128 bytes of weights and nt x 128 of
+//              tokens, 128-byte swizzle, an mbarrier ring
+//   warp 1     tcgen05.mma, M = 128 (256 on a pair of SMs), N = nt, K = 32 each
+//   warp 2     TMEM columns (up to four accumulators of nt columns)
+//   warps 4-11 epilogue: lane = channel, column = token; scales, rounding, stores
 #pragma once
 
 #include "sv_common.cuh"
@@ -477,10 +476,12 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NV <= 2 || (VEC == 1 && N
 
 // ----------------------------------------------------------------------------- the product
 
-constexpr int kQ8BM = 128;        // channels per tile = the MMA's M
-constexpr int kQ8BK = 128;        // K per stage: one 128-byte swizzled row of int8
-constexpr int kQ8MaxNT = 256;     // tokens per tile = the MMA's N
-constexpr int kQ8MaxStages = 12;
+constexpr int kQ8BM = 128;        // channels of a CTA's tile: the MMA's M, or half of it
+constexpr int kQ8BK = 128;        // K per block: one 128-byte swizzled row of int8
+constexpr int kQ8Sub = 2;         // K blocks per stage
+constexpr int kQ8MaxNT = 256;     // tokens of an accumulator = the MMA's N
+constexpr int kQ8MaxStages = 6;
+constexpr int kQ8MaxBufs = 4;     // accumulators in TMEM
 constexpr int kQ8EpiWarps = 8;    // per TMEM lane quarter two, on alternate 16-column chunks
 constexpr int kQ8Threads = 128 + 32 * kQ8EpiWarps;
 constexpr int kQ8SmemMax = 227 * 1024 - 1024;  // dynamic shared memory of one CTA (static part kept apart)
@@ -492,25 +493,81 @@ struct Q8GemmArgs {
     const float* w_scale;  // [V]
     int* err;              // optional: 1 if a wait gave up
     int M, V, K;
-    int nt;                // tokens per tile, a multiple of 16
+    int nt;                // tokens of an accumulator, a multiple of 16 (pairs: of 32)
+    int groups;            // accumulators of a tile (1 or 2): it has groups * nt tokens
+    int bufs;              // accumulators in TMEM, `buf_cols` columns each
+    int buf_cols, tmem_cols;
     int m_tiles, v_tiles;
     int stages;
-    int tmem_cols;         // a power of two, two accumulators
 };
 
-// Instruction descriptor: s32 accumulator, signed 8-bit A and B, both K-major.
-__device__ __forceinline__ uint32_t q8_idesc(int n)
+// Instruction descriptor: s32 accumulator, signed 8-bit A and B, both K-major, m x n.
+__device__ __forceinline__ uint32_t q8_idesc(int m, int n)
 {
-    return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kQ8BM >> 4) << 24);
+    return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
+template <bool PAIR>
 __device__ __forceinline__ void q8_mma(uint32_t tmem_d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t accumulate)
 {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, {%5, %6, %7, %8}, p;\n\t}" ::"r"(tmem_d),
-        "l"(da), "l"(db), "r"(idesc), "r"(accumulate), "r"(0u), "r"(0u), "r"(0u), "r"(0u));
+    if (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+            "l"(da), "l"(db), "r"(idesc), "r"(accumulate));
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+            "l"(da), "l"(db), "r"(idesc), "r"(accumulate));
+}
+
+// The barrier, in both CTAs of a pair, once this thread's MMAs so far are done.
+template <bool PAIR>
+__device__ __forceinline__ void q8_commit(uint64_t* bar)
+{
+    if (PAIR)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                         lr_smem(bar)),
+                     "h"((uint16_t)3)
+                     : "memory");
+    else
+        lr_commit(bar);
+}
+
+// To this CTA's shared memory; the bytes are counted by `bar`, in a pair the leader's.
+template <bool PAIR>
+__device__ __forceinline__ void q8_tma(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y)
+{
+    if (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+                lr_smem(dst)),
+            "l"((uint64_t)map), "r"(bar), "r"(x), "r"(y)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+                lr_smem(dst)),
+            "l"((uint64_t)map), "r"(bar), "r"(x), "r"(y)
+            : "memory");
+}
+
+// The leader's copy of a shared variable, as a cluster address (this CTA's own without a pair).
+template <bool PAIR>
+__device__ __forceinline__ uint32_t q8_leader(const void* p)
+{
+    uint32_t a = lr_smem(p);
+    if (PAIR) asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(lr_smem(p)));
+    return a;
+}
+
+__device__ __forceinline__ void q8_cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void q8_tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
@@ -527,7 +584,7 @@ __device__ __forceinline__ void q8_tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
 // The producer and the MMA issuer are whole warps in step, one elected lane of which
 // issues: addresses, descriptors and loop counts then live in uniform registers, where
 // the copies and MMAs want them (from one thread's registers every issue moved its
-// operands first, and a stage took Q8_SERIAL cycles whatever its products).
+// operands first).
 __device__ __forceinline__ bool q8_elect()
 {
     uint32_t p;
@@ -535,13 +592,16 @@ __device__ __forceinline__ bool q8_elect()
     return p != 0;
 }
 
-// lr_wait by a warp, one answer for all lanes
+// Wait by a warp, one answer for all lanes: the first look costs one vote.  False (after
+// raising the flags) if the phase did not complete within kLrPolls polls, or another
+// role of the CTA gave up.
 __device__ __forceinline__ bool q8_wait(uint64_t* bar, unsigned parity, volatile int* abort, int* err)
 {
+    if (__all_sync(0xffffffffu, lr_try_wait(bar, parity))) return true;
     return __all_sync(0xffffffffu, lr_wait(bar, parity, abort, err)) != 0;
 }
 
-// A place in the ring of stages and its phase: counted, not divided for.
+// A place in a ring and its phase: counted, not divided for.
 struct Q8Ring {
     int s = 0;
     unsigned phase = 0;
@@ -554,22 +614,37 @@ struct Q8Ring {
     }
 };
 
-// The logits of channel v (one a lane) and the tile's tokens, from the accumulator at
+// The logits of channel v (one a lane) and the accumulator's tokens m0 .., from TMEM at
 // acc: 16-column chunks grp, grp + 2, ...  A bf16 row of even length goes out in words:
 // two lanes trade a value, so each stores a channel pair of one of two tokens.
 template <int ESZ>
 __device__ __forceinline__ void q8_epilogue(const Q8GemmArgs& g, uint32_t acc, int grp, int m0, int v)
 {
     const float sw = v < g.V ? __ldg(g.w_scale + v) : 0.f;
+    const unsigned long long sw2 = pack2(sw, sw);
     const bool words = ESZ == 2 && (g.V & 1) == 0;
+    const bool wide = (reinterpret_cast<uintptr_t>(g.a_scale) & 15u) == 0;
     const int odd = v & 1;
     for (int c = grp * 16; c < g.nt && m0 + c < g.M; c += 32) {
+        const int left = g.M - (m0 + c);  // tokens from here on
+        float sa[16];
+        if (wide && left >= 16) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 4)
+                *reinterpret_cast<float4*>(sa + j) = __ldg(reinterpret_cast<const float4*>(g.a_scale + m0 + c + j));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sa[j] = j < left ? __ldg(g.a_scale + m0 + c + j) : 0.f;
+        }
         uint32_t r[16];
         q8_tmem_ld16(acc + (uint32_t)c, r);
         float z[16];
-        const int left = g.M - (m0 + c);  // tokens from here on
 #pragma unroll
-        for (int j = 0; j < 16; ++j) z[j] = (float)(int)r[j] * ((j < left ? __ldg(g.a_scale + m0 + c + j) : 0.f) * sw);
+        for (int j = 0; j < 16; j += 2) {
+            const unsigned long long p = pack2((float)(int)r[j], (float)(int)r[j + 1]);
+            unpack2(mul2(p, mul2(pack2(sa[j], sa[j + 1]), sw2)), z[j], z[j + 1]);
+        }
+        const bool in = v < g.V;  // (the others still take part in the loads and the trade)
         if (words) {
             uint32_t* to = static_cast<uint32_t*>(g.out) + ((size_t)(m0 + c + odd) * g.V + (v - odd)) / 2;
             const size_t step = (size_t)g.V;  // words of two rows
@@ -577,243 +652,72 @@ __device__ __forceinline__ void q8_epilogue(const Q8GemmArgs& g, uint32_t acc, i
             for (int j = 0; j < 16; j += 2) {
                 const float other = __shfl_xor_sync(0xffffffffu, odd ? z[j] : z[j + 1], 1);
                 const __nv_bfloat162 h = odd ? __floats2bfloat162_rn(other, z[j + 1]) : __floats2bfloat162_rn(z[j], other);
-                if (j + odd < left && v < g.V) *to = *reinterpret_cast<const uint32_t*>(&h);
+                if (j + odd < left && in) *to = *reinterpret_cast<const uint32_t*>(&h);
                 to += step;
             }
         } else {
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-                if (j < left && v < g.V) q8_st1<ESZ>(g.out, (size_t)(m0 + c + j) * g.V + v, z[j]);
+                if (j < left && in) q8_st1<ESZ>(g.out, (size_t)(m0 + c + j) * g.V + v, z[j]);
         }
     }
 }
 
-// Persistent, one CTA per SM; tiles blockIdx.x, blockIdx.x + gridDim.x, ... with
-// the token tile fastest, so the CTAs that share weights run at about the same time.
-// Every wait on an mbarrier is bounded: past kLrPolls polls the CTA raises *err,
-// stops issuing, and still frees its TMEM.
-template <int ESZ>
+// Persistent, one CTA per SM, or a pair of them (PAIR: cta_group::2) on one tile of 256
+// channels: each CTA holds its 128 channels and HALF the tokens, and gets all of the
+// tile's columns for its channels, so an SM's shared memory is filled and read with two
+// thirds of the bytes a product.  The pair's leader waits, issues and commits for both.
+// Tiles are walked with the token tile fastest, so those that share weights run at about
+// the same time.  A tile of two accumulators (groups = 2) reads its weights once for both.
+// Every wait on an mbarrier is bounded: past kLrPolls polls the CTA raises *err, stops
+// issuing, and still frees its TMEM.
+template <int ESZ, bool PAIR>
 __global__ void __launch_bounds__(kQ8Threads, 1)
     sv_q8_gemm(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap ta, Q8GemmArgs g)
 {
     extern __shared__ unsigned char q8_dyn[];
-    // every stage starts on a 1024-byte boundary of the shared window (the swizzle atom)
+    // every block on a 1024-byte boundary of the shared window (the swizzle atom)
     unsigned char* ring = q8_dyn + ((1024u - (lr_smem(q8_dyn) & 1023u)) & 1023u);
-    __shared__ __align__(8) uint64_t full[kQ8MaxStages], empty[kQ8MaxStages], tfull[2], tempty[2];
-    __shared__ uint32_t s_tmem;
-    __shared__ int s_abort, s_consumed;
-
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int kbs = (g.K + kQ8BK - 1) / kQ8BK, S = g.stages;
-    const int STAGE = kQ8WBytes + g.nt * kQ8BK;
-    const long long tiles = (long long)g.m_tiles * g.v_tiles;
-
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < S; ++s) {
-            lr_mbar_init(&full[s], 1);
-            lr_mbar_init(&empty[s], 1);
-        }
-        for (int b = 0; b < 2; ++b) {
-            lr_mbar_init(&tfull[b], 1);
-            lr_mbar_init(&tempty[b], kQ8EpiWarps);
-        }
-        s_abort = 0;
-        s_consumed = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    if (warp == 2) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(lr_smem(&s_tmem)),
-                     "r"(g.tmem_cols));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    }
-    lr_fence_before();
-    __syncthreads();
-    lr_fence_after();
-    const uint32_t tmem = s_tmem;
-    volatile int* abort = &s_abort;
-
-    int issued = 0;
-    if (warp == 0) {
-        // ---- producer: one global count of stages across the CTA's tiles
-        Q8Ring r;
-        bool ok = true;
-        for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-            const int m0 = (int)(t % g.m_tiles) * g.nt, v0 = (int)(t / g.m_tiles) * kQ8BM;
-            for (int kb = 0; kb < kbs; ++kb) {
-                if (issued >= S && !q8_wait(&empty[r.s], r.phase ^ 1u, abort, g.err)) { ok = false; break; }
-                if (q8_elect()) {
-                    unsigned char* st = ring + r.s * STAGE;
-                    lr_expect_tx(&full[r.s], (unsigned)STAGE);
-                    lr_tma_2d(st, &tw, &full[r.s], kb * kQ8BK, v0);
-                    lr_tma_2d(st + kQ8WBytes, &ta, &full[r.s], kb * kQ8BK, m0);
-                }
-                __syncwarp();
-                ++issued;
-                r.next(S);
-            }
-        }
-    } else if (warp == 1) {
-        // ---- MMA issuer
-        const uint32_t idesc = q8_idesc(g.nt);
-        const uint64_t wd0 = lr_desc(lr_smem(ring)), ad0 = lr_desc(lr_smem(ring) + kQ8WBytes);
-        Q8Ring r;
-        int consumed = 0, i = 0;
-        bool ok = true;
-        for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++i) {
-            const int b = i & 1, use = i >> 1;
-            if (use >= 1 && !q8_wait(&tempty[b], (unsigned)(use - 1) & 1u, abort, g.err)) break;
-            lr_fence_after();
-            const uint32_t d = tmem + (uint32_t)(b * (g.tmem_cols / 2));
-            for (int kb = 0; kb < kbs; ++kb) {
-                if (!q8_wait(&full[r.s], r.phase, abort, g.err)) { ok = false; break; }
-                lr_fence_after();
-                if (q8_elect()) {
-                    const uint64_t off = (uint64_t)((unsigned)(r.s * STAGE) >> 4);
-#pragma unroll
-                    for (int j = 0; j < kQ8BK / 32; ++j)  // K = 32 per MMA: 32 bytes along the swizzled row
-                        q8_mma(d, wd0 + off + 2 * j, ad0 + off + 2 * j, idesc, (kb > 0 || j > 0) ? 1u : 0u);
-                    lr_commit(&empty[r.s]);
-                }
-                __syncwarp();
-                ++consumed;
-                r.next(S);
-            }
-            if (ok && q8_elect()) lr_commit(&tfull[b]);
-            __syncwarp();
-        }
-        if (lane == 0) s_consumed = consumed;
-    } else if (warp >= 4) {
-        // ---- epilogue: warp 4 + e owns TMEM lanes (= channels of the tile) 32q .. 32q + 31,
-        // q = e % 4, and the 16-column chunks e / 4, e / 4 + 2, ...
-        const int q = (warp - 4) & 3, grp = (warp - 4) >> 2;
-        int i = 0;
-        for (long long t = blockIdx.x; t < tiles; t += gridDim.x, ++i) {
-            const int b = i & 1, use = i >> 1;
-            const int m0 = (int)(t % g.m_tiles) * g.nt;
-            const int v = (int)(t / g.m_tiles) * kQ8BM + 32 * q + lane;
-            // one lane waits, so the warp-wide tcgen05.ld below runs on all lanes or none
-            int ready = 0;
-            if (lane == 0) ready = lr_wait(&tfull[b], (unsigned)use & 1u, abort, g.err) ? 1 : 0;
-            ready = __shfl_sync(0xffffffffu, ready, 0);
-            if (!ready) break;
-            lr_fence_after();
-            const uint32_t acc = tmem + (uint32_t)(b * (g.tmem_cols / 2)) + ((uint32_t)(32 * q) << 16);
-            q8_epilogue<ESZ>(g, acc, grp, m0, v);
-            lr_fence_before();
-            __syncwarp();
-            if (lane == 0) lr_arrive(&tempty[b]);
-        }
-    }
-    lr_fence_before();
-    __syncthreads();
-    // after a wait gave up: let the copies this CTA issued but never consumed land
-    // (bounded) before its shared memory goes away
-    if (warp == 0 && lane == 0 && s_abort) {
-        for (int it = s_consumed; it < issued; ++it) {
-            const unsigned par = (unsigned)(it / S) & 1u;
-            for (unsigned k = 0; k < kLrPolls && !lr_try_wait(&full[it % S], par); ++k) {
-            }
-        }
-    }
-    if (warp == 2) {
-        lr_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(g.tmem_cols));
-    }
-}
-
-// ---- pairs of CTAs (cta_group::2): one MMA of M = 256 over two SMs.  Each CTA holds its
-// 128 channels and HALF the tokens of the tile, and gets all of the tile's columns for its
-// channels, so an SM's shared memory is filled and read with two thirds of the bytes a
-// product (nt = 256: 8 KB read an MMA and 32 KB filled a stage, against 12 and 48).
-// rank 0 of the cluster waits, issues and commits for both.
-
-__device__ __forceinline__ uint32_t q8_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-// the address of the leader's copy of a shared variable
-__device__ __forceinline__ uint32_t q8_leader(const void* p)
-{
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(lr_smem(p)));
-    return a;
-}
-
-// to this CTA's shared memory, counted by the leader's barrier
-__device__ __forceinline__ void q8_tma_pair(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
-            lr_smem(dst)),
-        "l"((uint64_t)map), "r"(bar), "r"(x), "r"(y)
-        : "memory");
-}
-
-__device__ __forceinline__ void q8_mma_pair(uint32_t tmem_d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t accumulate)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
-        "l"(da), "l"(db), "r"(idesc), "r"(accumulate));
-}
-
-// both CTAs' copies of a barrier, once this thread's MMAs are done
-__device__ __forceinline__ void q8_commit_pair(uint64_t* bar)
-{
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-                     lr_smem(bar)),
-                 "h"((uint16_t)3)
-                 : "memory");
-}
-
-__device__ __forceinline__ void q8_cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-template <int ESZ>
-__global__ void __launch_bounds__(kQ8Threads, 1)
-    sv_q8_gemm_pair(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap ta, Q8GemmArgs g)
-{
-    extern __shared__ unsigned char q8_dyn[];
-    // the same offset in both CTAs, every stage on a 1024-byte boundary of the shared window
-    unsigned char* ring = q8_dyn + ((1024u - (lr_smem(q8_dyn) & 1023u)) & 1023u);
-    __shared__ __align__(8) uint64_t full[kQ8MaxStages], empty[kQ8MaxStages], tfull[2], tempty[2];
+    __shared__ __align__(8) uint64_t full[kQ8MaxStages], empty[kQ8MaxStages], tfull[kQ8MaxBufs], tempty[kQ8MaxBufs];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)q8_rank();
-    const int kbs = (g.K + kQ8BK - 1) / kQ8BK, S = g.stages, half = g.nt / 2;
-    const int STAGE = kQ8WBytes + half * kQ8BK;
-    const long long tiles = (long long)g.m_tiles * g.v_tiles;  // v_tiles of 256 channels
-    const long long pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    constexpr int CTAS = PAIR ? 2 : 1;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    int rank = 0;
+    if (PAIR) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    const int kbs = (g.K + kQ8BK - 1) / kQ8BK, S = g.stages, G = g.groups;
+    const int mine = g.nt / CTAS, a_bytes = mine * kQ8BK;  // this CTA's tokens of an accumulator
+    const int BLOCK = kQ8WBytes + G * a_bytes, STAGE = kQ8Sub * BLOCK;
+    const long long tiles = (long long)g.m_tiles * g.v_tiles;
+    const long long first = blockIdx.x / CTAS, step = gridDim.x / CTAS;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             lr_mbar_init(&full[s], 1);
             lr_mbar_init(&empty[s], 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < g.bufs; ++b) {
             lr_mbar_init(&tfull[b], 1);
-            lr_mbar_init(&tempty[b], 2 * kQ8EpiWarps);
+            lr_mbar_init(&tempty[b], CTAS * kQ8EpiWarps);
         }
         s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 2) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(lr_smem(&s_tmem)),
-                     "r"(g.tmem_cols));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        if (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(lr_smem(&s_tmem)),
+                         "r"(g.tmem_cols));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(lr_smem(&s_tmem)),
+                         "r"(g.tmem_cols));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        }
     }
     lr_fence_before();
     __syncthreads();
-    q8_cluster_sync();  // both CTAs' barriers stand before either is reached from the other
+    if (PAIR) q8_cluster_sync();  // both CTAs' barriers stand before either is reached from the other
     lr_fence_after();
     const uint32_t tmem = s_tmem;
     volatile int* abort = &s_abort;
@@ -823,16 +727,22 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         Q8Ring r;
         int it = 0;
         bool ok = true;
-        const uint32_t bars = q8_leader(full);
-        for (long long t = pair; ok && t < tiles; t += pairs) {
-            const int m0 = (int)(t % g.m_tiles) * g.nt + rank * half, v0 = (int)(t / g.m_tiles) * 2 * kQ8BM + rank * kQ8BM;
-            for (int kb = 0; kb < kbs; ++kb) {
+        const uint32_t bars = q8_leader<PAIR>(full);
+        for (long long t = first; ok && t < tiles; t += step) {
+            const int m0 = (int)(t % g.m_tiles) * G * g.nt + rank * mine;
+            const int v0 = ((int)(t / g.m_tiles) * CTAS + rank) * kQ8BM;
+            for (int kb = 0; kb < kbs; kb += kQ8Sub) {
                 if (it >= S && !q8_wait(&empty[r.s], r.phase ^ 1u, abort, g.err)) { ok = false; break; }
                 if (q8_elect()) {
                     unsigned char* st = ring + r.s * STAGE;
-                    if (rank == 0) lr_expect_tx(&full[r.s], 2u * (unsigned)STAGE);
-                    q8_tma_pair(st, &tw, bars + 8u * r.s, kb * kQ8BK, v0);
-                    q8_tma_pair(st + kQ8WBytes, &ta, bars + 8u * r.s, kb * kQ8BK, m0);
+                    const uint32_t bar = bars + 8u * r.s;
+                    const int subs = min(kQ8Sub, kbs - kb);
+                    if (rank == 0) lr_expect_tx(&full[r.s], (unsigned)(CTAS * subs * BLOCK));
+                    for (int u = 0; u < subs; ++u, st += BLOCK) {
+                        q8_tma<PAIR>(st, &tw, bar, (kb + u) * kQ8BK, v0);
+                        q8_tma<PAIR>(st + kQ8WBytes, &ta, bar, (kb + u) * kQ8BK, m0);
+                        if (G > 1) q8_tma<PAIR>(st + kQ8WBytes + a_bytes, &ta, bar, (kb + u) * kQ8BK, m0 + g.nt);
+                    }
                 }
                 __syncwarp();
                 ++it;
@@ -842,53 +752,73 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         // every stage handed back: nothing of the pair's is still on its way to this CTA
         for (int u = max(0, it - S); ok && u < it; ++u) ok = q8_wait(&empty[u % S], (unsigned)(u / S) & 1u, abort, g.err);
     } else if (warp == 1 && rank == 0) {
-        // ---- MMA issuer of the pair
-        const uint32_t idesc = (q8_idesc(g.nt) & ~(31u << 24)) | ((uint32_t)(2 * kQ8BM >> 4) << 24);
-        const uint64_t wd0 = lr_desc(lr_smem(ring)), ad0 = lr_desc(lr_smem(ring) + kQ8WBytes);
-        Q8Ring r;
-        int i = 0;
+        // ---- MMA issuer
+        const uint32_t idesc = q8_idesc(CTAS * kQ8BM, g.nt);
+        const uint64_t w0 = lr_desc(lr_smem(ring)), a_off = kQ8WBytes >> 4, g_off = (uint64_t)(a_bytes >> 4);
+        Q8Ring r, acc;
+        int used = 0;  // accumulators so far, up to g.bufs
         bool ok = true;
-        for (long long t = pair; ok && t < tiles; t += pairs, ++i) {
-            const int b = i & 1, use = i >> 1;
-            if (use >= 1 && !q8_wait(&tempty[b], (unsigned)(use - 1) & 1u, abort, g.err)) break;
+        for (long long t = first; ok && t < tiles; t += step) {
+            uint32_t d[2];
+            int buf[2];
+            for (int h = 0; h < G; ++h) {
+                buf[h] = acc.s;
+                d[h] = tmem + (uint32_t)(acc.s * g.buf_cols);
+                if (used >= g.bufs) ok = ok && q8_wait(&tempty[acc.s], acc.phase ^ 1u, abort, g.err);
+                else ++used;
+                acc.next(g.bufs);
+            }
+            if (!ok) break;
             lr_fence_after();
-            const uint32_t d = tmem + (uint32_t)(b * (g.tmem_cols / 2));
-            for (int kb = 0; kb < kbs; ++kb) {
+            for (int kb = 0; kb < kbs; kb += kQ8Sub) {
                 if (!q8_wait(&full[r.s], r.phase, abort, g.err)) { ok = false; break; }
                 lr_fence_after();
                 if (q8_elect()) {
-                    const uint64_t off = (uint64_t)((unsigned)(r.s * STAGE) >> 4);
+                    uint64_t w = w0 + (uint64_t)((unsigned)(r.s * STAGE) >> 4);
 #pragma unroll
-                    for (int j = 0; j < kQ8BK / 32; ++j)
-                        q8_mma_pair(d, wd0 + off + 2 * j, ad0 + off + 2 * j, idesc, (kb > 0 || j > 0) ? 1u : 0u);
-                    q8_commit_pair(&empty[r.s]);
+                    for (int u = 0; u < kQ8Sub; ++u, w += (unsigned)BLOCK >> 4) {
+                        if (kb + u >= kbs) break;
+#pragma unroll
+                        for (int j = 0; j < kQ8BK / 32; ++j) {  // K = 32 per MMA: 32 bytes along the swizzled row
+                            const uint32_t on = (kb + u > 0 || j > 0) ? 1u : 0u;
+                            q8_mma<PAIR>(d[0], w + 2 * j, w + a_off + 2 * j, idesc, on);
+                            if (G > 1) q8_mma<PAIR>(d[1], w + 2 * j, w + a_off + g_off + 2 * j, idesc, on);
+                        }
+                    }
+                    q8_commit<PAIR>(&empty[r.s]);
                 }
                 __syncwarp();
                 r.next(S);
             }
-            if (ok && q8_elect()) q8_commit_pair(&tfull[b]);
+            if (ok && q8_elect())
+                for (int h = 0; h < G; ++h) q8_commit<PAIR>(&tfull[buf[h]]);
             __syncwarp();
         }
     } else if (warp >= 4) {
-        // ---- epilogue of this CTA's 128 channels, as sv_q8_gemm's
+        // ---- epilogue: warp 4 + e owns TMEM lanes (= this CTA's channels) 32q .. 32q + 31,
+        // q = e % 4, and the 16-column chunks e / 4, e / 4 + 2, ...
         const int q = (warp - 4) & 3, grp = (warp - 4) >> 2;
-        int i = 0;
-        for (long long t = pair; t < tiles; t += pairs, ++i) {
-            const int b = i & 1, use = i >> 1;
-            const int m0 = (int)(t % g.m_tiles) * g.nt;
-            const int v = (int)(t / g.m_tiles) * 2 * kQ8BM + rank * kQ8BM + 32 * q + lane;
-            int ready = 0;
-            if (lane == 0) ready = lr_wait(&tfull[b], (unsigned)use & 1u, abort, g.err) ? 1 : 0;
-            ready = __shfl_sync(0xffffffffu, ready, 0);
-            if (!ready) break;
-            lr_fence_after();
-            q8_epilogue<ESZ>(g, tmem + (uint32_t)(b * (g.tmem_cols / 2)) + ((uint32_t)(32 * q) << 16), grp, m0, v);
-            lr_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(q8_leader(&tempty[b])) : "memory");
+        Q8Ring acc;
+        bool ok = true;
+        for (long long t = first; ok && t < tiles; t += step) {
+            const int m0 = (int)(t % g.m_tiles) * G * g.nt;
+            const int v = ((int)(t / g.m_tiles) * CTAS + rank) * kQ8BM + 32 * q + lane;
+            for (int h = 0; h < G; ++h) {
+                // the warp-wide tcgen05.ld below runs on all lanes or none
+                ok = q8_wait(&tfull[acc.s], acc.phase, abort, g.err);
+                if (!ok) break;
+                lr_fence_after();
+                q8_epilogue<ESZ>(g, tmem + (uint32_t)(acc.s * g.buf_cols) + ((uint32_t)(32 * q) << 16), grp, m0 + h * g.nt, v);
+                lr_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(q8_leader<PAIR>(&tempty[acc.s]))
+                                 : "memory");
+                acc.next(g.bufs);
+            }
         }
     }
+    __syncwarp();
     // after a wait gave up: time for the copies in flight to land before the memory goes
     // away (two milliseconds, a thousand times what one takes)
     if (threadIdx.x == 0 && s_abort) {
@@ -902,10 +832,11 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     }
     lr_fence_before();
     __syncthreads();
-    q8_cluster_sync();  // neither CTA leaves while the other may still reach its barriers
+    if (PAIR) q8_cluster_sync();  // neither CTA leaves while the other may still reach its barriers
     if (warp == 2) {
         lr_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(g.tmem_cols));
+        if (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(g.tmem_cols));
+        else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(g.tmem_cols));
     }
 }
 
