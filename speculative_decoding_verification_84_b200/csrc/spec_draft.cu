@@ -7,8 +7,6 @@
 #include <cuda.h>  // CUtensorMap: driver calls go through entry points
 #include <cuda_runtime.h>
 #include <stdint.h>
-#include <stdlib.h>
-#include <stdio.h>
 
 #include <algorithm>
 #include <atomic>
@@ -126,57 +124,98 @@ bool q8_map(CUtensorMap* m, const void* base, long long rows, long long K, long 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Whether the product runs on pairs of SMs.
-bool q8_pairs(const Q8GemmArgs& g)
+// Pairs of SMs resident at once on the current device (an SM without a partner in its
+// GPC has none); 0 and *e on a CUDA error.
+template <int ESZ>
+int q8_resident_pairs(cudaError_t* e)
 {
-    static const char* force = getenv("Q8P");
-    if (force) return force[0] == '1';
-    return g.M > 64;
+    static std::atomic<int> resident[kMaxDevices];
+    static std::atomic<bool> ready[kMaxDevices];
+    if ((*e = allow_smem(sv_q8_gemm<ESZ, true>, kQ8SmemMax, ready)) != cudaSuccess) return 0;
+    int dev = 0;
+    if ((*e = cudaGetDevice(&dev)) != cudaSuccess) return 0;
+    const bool known = dev >= 0 && dev < kMaxDevices;
+    int n = known ? resident[dev].load(std::memory_order_relaxed) : 0;
+    if (n) return n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * (device_sm_count() / 2)));
+    cfg.blockDim = dim3(kQ8Threads);
+    cfg.dynamicSmemBytes = kQ8SmemMax;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    *e = cudaOccupancyMaxActiveClusters(&n, sv_q8_gemm<ESZ, true>, &cfg);
+    if (*e == cudaSuccess && n < 1) *e = cudaErrorInvalidConfiguration;
+    if (*e != cudaSuccess) return 0;
+    if (known) resident[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
 
-int q8_groups(const Q8GemmArgs& g, long long accs)
+// How the product is cut.
+//  * Pairs of SMs where an SM has 32 K blocks or more to walk; the pair's extra steps at
+//    start and end cost about 1.3 us (37 x 1001 x 3001: 6.5 us on single SMs, 8.0 on
+//    pairs; 1 x 4096 x 32000: 24.5 and 23.9; 2048 x 4096 x 64000: 441 and 384).
+//  * As few accumulators of 256 tokens as hold the batch, all of one size; more and
+//    smaller ones where the tiles would leave SMs idle.
+//  * Two accumulators to a tile where they are the whole batch, so that the weights are
+//    read once, if a third fits beside them (the next tile then starts while these are
+//    stored: at most 160 tokens each) and the rounds of tiles are not made worse by it: a
+//    tile of two takes 1.8 times as long (320 x 4096: V = 128256 7 rounds 140 us against
+//    14 of 156; V = 64000 4 of 82 against 7 of 81).
+//  * Two K blocks to a stage where four such stages fit, which halves the waits and
+//    commits; else one (2048 x 4096 x 64000: 384 us with one, 398 with two; 1 x 4096 x
+//    64000: 46.0 and 44.3).
+void q8_cut(Q8GemmArgs& g, int sms, int resident, bool* pairs)
 {
-    static const char* force = getenv("Q8G");
-    if (force) return accs > 1 ? force[0] - '0' : 1;
-    return accs == 2 ? 2 : 1;
+    const int kbs = (int)cdiv(g.K, kQ8BK);
+    const long long accs = cdiv(g.M, kQ8MaxNT);
+    *pairs = cdiv(accs * cdiv(g.V, 2 * kQ8BM), resident) * kbs >= 32;
+    const int unit = *pairs ? 32 : 16;
+    const long long units = *pairs ? resident : sms;  // tiles at a time
+    g.v_tiles = (int)cdiv(g.V, *pairs ? 2 * kQ8BM : kQ8BM);
+    long long parts = accs;
+    if (parts * g.v_tiles < units) parts = std::min<long long>(units / g.v_tiles, std::max<long long>(accs, cdiv(g.M, 32)));
+    g.nt = (int)(cdiv(cdiv(g.M, parts), unit) * unit);
+    parts = cdiv(g.M, g.nt);
+    g.groups = 1;
+    if (*pairs && parts == 2 && g.nt <= 160 && 9 * cdiv(g.v_tiles, units) < 5 * cdiv(2LL * g.v_tiles, units)) g.groups = 2;
+    g.m_tiles = (int)cdiv(parts, g.groups);
+    g.buf_cols = (int)(cdiv(g.nt, 32) * 32);
+    g.bufs = std::min(kQ8MaxBufs, 512 / g.buf_cols);
+    g.tmem_cols = 32;
+    while (g.tmem_cols < g.bufs * g.buf_cols) g.tmem_cols *= 2;
+    const int block = kQ8WBytes + g.groups * (*pairs ? g.nt / 2 : g.nt) * kQ8BK;
+    g.sub = 4 * kQ8MaxSub * block <= kQ8SmemMax - 1024 ? kQ8MaxSub : 1;
+    g.stages = std::min(kQ8MaxStages, (kQ8SmemMax - 1024) / (g.sub * block));
 }
 
 template <int ESZ>
 cudaError_t q8_gemm_launch(const void* a, long long lda, const void* w, long long ldw, Q8GemmArgs g, cudaStream_t st)
 {
-    const int sms = device_sm_count();
-    const bool pairs = q8_pairs(g);
-    // as few accumulators of 256 tokens as hold the batch, all of one size; two to a tile
-    // where that is the whole batch (the weights are then read once)
-    const int unit = pairs ? 32 : 16;
-    const long long accs = cdiv(g.M, kQ8MaxNT);
-    g.nt = (int)(cdiv(cdiv(g.M, accs), unit) * unit);
-    g.groups = q8_groups(g, accs);
-    g.m_tiles = (int)cdiv(g.M, (long long)g.nt * g.groups);
-    g.v_tiles = (int)cdiv(g.V, pairs ? 2 * kQ8BM : kQ8BM);
-    g.buf_cols = (int)(cdiv(g.nt, 32) * 32);
-    g.bufs = std::min(kQ8MaxBufs, 512 / g.buf_cols);
-    g.tmem_cols = 32;
-    while (g.tmem_cols < g.bufs * g.buf_cols) g.tmem_cols *= 2;
+    cudaError_t e;
+    const int sms = device_sm_count(), resident = q8_resident_pairs<ESZ>(&e);
+    if (e != cudaSuccess) return e;
+    bool pairs;
+    q8_cut(g, sms, resident, &pairs);
     const int mine = pairs ? g.nt / 2 : g.nt;  // tokens of an accumulator in one CTA
-    const int stage = kQ8Sub * (kQ8WBytes + g.groups * mine * kQ8BK);
-    g.stages = std::min(kQ8MaxStages, (kQ8SmemMax - 1024) / stage);
     CUtensorMap tw, ta;
     if (!q8_map(&tw, w, g.V, g.K, ldw, kQ8BM) || !q8_map(&ta, a, g.M, g.K, lda, mine)) return cudaErrorInvalidValue;
     const long long tiles = (long long)g.m_tiles * g.v_tiles;
-    const int smem = 1024 + g.stages * stage;
-    static std::atomic<bool> ready[kMaxDevices], ready2[kMaxDevices];
+    const size_t smem = 1024 + (size_t)g.stages * g.sub * (kQ8WBytes + g.groups * mine * kQ8BK);
     if (!pairs) {
-        const cudaError_t e = allow_smem(sv_q8_gemm<ESZ, false>, kQ8SmemMax, ready);
-        if (e != cudaSuccess) return e;
+        static std::atomic<bool> ready[kMaxDevices];
+        if ((e = allow_smem(sv_q8_gemm<ESZ, false>, kQ8SmemMax, ready)) != cudaSuccess) return e;
         sv_q8_gemm<ESZ, false><<<(unsigned)std::min<long long>(tiles, sms), kQ8Threads, smem, st>>>(tw, ta, g);
         return cudaGetLastError();
     }
-    cudaError_t e = allow_smem(sv_q8_gemm<ESZ, true>, kQ8SmemMax, ready2);
-    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * std::min<long long>(tiles, resident)));
     cfg.blockDim = dim3(kQ8Threads);
-    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -185,20 +224,6 @@ cudaError_t q8_gemm_launch(const void* a, long long lda, const void* w, long lon
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    // as many pairs as are resident at once (an SM without a partner in its GPC has none)
-    static std::atomic<int> resident[kMaxDevices];
-    int dev = 0;
-    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-    int n = dev >= 0 && dev < kMaxDevices ? resident[dev].load(std::memory_order_relaxed) : 0;
-    if (!n) {
-        cfg.gridDim = dim3((unsigned)(2 * (sms / 2)));
-        cfg.dynamicSmemBytes = kQ8SmemMax;
-        if ((e = cudaOccupancyMaxActiveClusters(&n, sv_q8_gemm<ESZ, true>, &cfg)) != cudaSuccess) return e;
-        if (n < 1) return cudaErrorInvalidConfiguration;
-        cfg.dynamicSmemBytes = (size_t)smem;
-        if (dev >= 0 && dev < kMaxDevices) resident[dev].store(n, std::memory_order_relaxed);
-    }
-    cfg.gridDim = dim3((unsigned)(2 * std::min<long long>(tiles, n)));
     return cudaLaunchKernelEx(&cfg, sv_q8_gemm<ESZ, true>, tw, ta, g);
 }
 

@@ -478,9 +478,9 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NV <= 2 || (VEC == 1 && N
 
 constexpr int kQ8BM = 128;        // channels of a CTA's tile: the MMA's M, or half of it
 constexpr int kQ8BK = 128;        // K per block: one 128-byte swizzled row of int8
-constexpr int kQ8Sub = 2;         // K blocks per stage
+constexpr int kQ8MaxSub = 2;      // K blocks per stage
 constexpr int kQ8MaxNT = 256;     // tokens of an accumulator = the MMA's N
-constexpr int kQ8MaxStages = 6;
+constexpr int kQ8MaxStages = 8;
 constexpr int kQ8MaxBufs = 4;     // accumulators in TMEM
 constexpr int kQ8EpiWarps = 8;    // per TMEM lane quarter two, on alternate 16-column chunks
 constexpr int kQ8Threads = 128 + 32 * kQ8EpiWarps;
@@ -498,7 +498,7 @@ struct Q8GemmArgs {
     int bufs;              // accumulators in TMEM, `buf_cols` columns each
     int buf_cols, tmem_cols;
     int m_tiles, v_tiles;
-    int stages;
+    int stages, sub;       // of `sub` K blocks each
 };
 
 // Instruction descriptor: s32 accumulator, signed 8-bit A and B, both K-major, m x n.
@@ -688,7 +688,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     if (PAIR) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     const int kbs = (g.K + kQ8BK - 1) / kQ8BK, S = g.stages, G = g.groups;
     const int mine = g.nt / CTAS, a_bytes = mine * kQ8BK;  // this CTA's tokens of an accumulator
-    const int BLOCK = kQ8WBytes + G * a_bytes, STAGE = kQ8Sub * BLOCK;
+    const int BLOCK = kQ8WBytes + G * a_bytes, SUB = g.sub, STAGE = SUB * BLOCK;
     const long long tiles = (long long)g.m_tiles * g.v_tiles;
     const long long first = blockIdx.x / CTAS, step = gridDim.x / CTAS;
 
@@ -731,12 +731,12 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         for (long long t = first; ok && t < tiles; t += step) {
             const int m0 = (int)(t % g.m_tiles) * G * g.nt + rank * mine;
             const int v0 = ((int)(t / g.m_tiles) * CTAS + rank) * kQ8BM;
-            for (int kb = 0; kb < kbs; kb += kQ8Sub) {
+            for (int kb = 0; kb < kbs; kb += SUB) {
                 if (it >= S && !q8_wait(&empty[r.s], r.phase ^ 1u, abort, g.err)) { ok = false; break; }
                 if (q8_elect()) {
                     unsigned char* st = ring + r.s * STAGE;
                     const uint32_t bar = bars + 8u * r.s;
-                    const int subs = min(kQ8Sub, kbs - kb);
+                    const int subs = min(SUB, kbs - kb);
                     if (rank == 0) lr_expect_tx(&full[r.s], (unsigned)(CTAS * subs * BLOCK));
                     for (int u = 0; u < subs; ++u, st += BLOCK) {
                         q8_tma<PAIR>(st, &tw, bar, (kb + u) * kQ8BK, v0);
@@ -770,14 +770,14 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
             }
             if (!ok) break;
             lr_fence_after();
-            for (int kb = 0; kb < kbs; kb += kQ8Sub) {
+            for (int kb = 0; kb < kbs; kb += SUB) {
                 if (!q8_wait(&full[r.s], r.phase, abort, g.err)) { ok = false; break; }
                 lr_fence_after();
                 if (q8_elect()) {
                     uint64_t w = w0 + (uint64_t)((unsigned)(r.s * STAGE) >> 4);
 #pragma unroll
-                    for (int u = 0; u < kQ8Sub; ++u, w += (unsigned)BLOCK >> 4) {
-                        if (kb + u >= kbs) break;
+                    for (int u = 0; u < kQ8MaxSub; ++u, w += (unsigned)BLOCK >> 4) {
+                        if (u >= SUB || kb + u >= kbs) break;
 #pragma unroll
                         for (int j = 0; j < kQ8BK / 32; ++j) {  // K = 32 per MMA: 32 bytes along the swizzled row
                             const uint32_t on = (kb + u > 0 || j > 0) ? 1u : 0u;
