@@ -21,7 +21,7 @@
 //              tokens, 128-byte swizzle, an mbarrier ring
 //   warp 1     tcgen05.mma, M = 128 (256 on a pair of SMs), N = nt, K = 32 each
 //   warp 2     TMEM columns (up to four accumulators of nt columns)
-//   warps 4-11 epilogue: lane = channel, column = token; scales, rounding, stores
+//   warps 4-19 epilogue: lane = channel, column = token; scales, rounding, stores
 #pragma once
 
 #include "sv_common.cuh"
@@ -482,7 +482,7 @@ constexpr int kQ8MaxSub = 2;      // K blocks per stage
 constexpr int kQ8MaxNT = 256;     // tokens of an accumulator = the MMA's N
 constexpr int kQ8MaxStages = 8;
 constexpr int kQ8MaxBufs = 4;     // accumulators in TMEM
-constexpr int kQ8EpiWarps = 8;    // per TMEM lane quarter two, on alternate 16-column chunks
+constexpr int kQ8EpiWarps = 16;   // per TMEM lane quarter four, on every fourth 16-column chunk
 constexpr int kQ8Threads = 128 + 32 * kQ8EpiWarps;
 constexpr int kQ8SmemMax = 227 * 1024 - 1024;  // dynamic shared memory of one CTA (static part kept apart)
 constexpr int kQ8WBytes = kQ8BM * kQ8BK;
@@ -615,7 +615,7 @@ struct Q8Ring {
 };
 
 // The logits of channel v (one a lane) and the accumulator's tokens m0 .., from TMEM at
-// acc: 16-column chunks grp, grp + 2, ...  A bf16 row of even length goes out in words:
+// acc: 16-column chunks grp, grp + 4, ...  A bf16 row of even length goes out in words:
 // two lanes trade a value, so each stores a channel pair of one of two tokens.
 template <int ESZ>
 __device__ __forceinline__ void q8_epilogue(const Q8GemmArgs& g, uint32_t acc, int grp, int m0, int v)
@@ -625,7 +625,7 @@ __device__ __forceinline__ void q8_epilogue(const Q8GemmArgs& g, uint32_t acc, i
     const bool words = ESZ == 2 && (g.V & 1) == 0;
     const bool wide = (reinterpret_cast<uintptr_t>(g.a_scale) & 15u) == 0;
     const int odd = v & 1;
-    for (int c = grp * 16; c < g.nt && m0 + c < g.M; c += 32) {
+    for (int c = grp * 16; c < g.nt && m0 + c < g.M; c += 4 * kQ8EpiWarps) {
         const int left = g.M - (m0 + c);  // tokens from here on
         float sa[16];
         if (wide && left >= 16) {
@@ -796,7 +796,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         }
     } else if (warp >= 4) {
         // ---- epilogue: warp 4 + e owns TMEM lanes (= this CTA's channels) 32q .. 32q + 31,
-        // q = e % 4, and the 16-column chunks e / 4, e / 4 + 2, ...
+        // q = e % 4, and the 16-column chunks e / 4, e / 4 + 4, ...
         const int q = (warp - 4) & 3, grp = (warp - 4) >> 2;
         Q8Ring acc;
         bool ok = true;
