@@ -41,16 +41,16 @@ cudaError_t allow_smem(Kernel kernel, int bytes, std::atomic<bool> (&ready)[kMax
 
 constexpr int kQ8RowsSmemMax = 200 * 1024;  // three rows of x and of the residual
 
-template <int ESZ, int VEC, int NV, int MAXT>
-cudaError_t q8_rows_go(const Q8RowsArgs& g, int threads, cudaStream_t st)
+template <int ESZ, int VEC, int NV, int MAXT, bool RES>
+cudaError_t q8_rows_res(const Q8RowsArgs& g, int threads, cudaStream_t st)
 {
     // rows of one warp: eight to a CTA
     const dim3 block(threads, threads == 32 ? 8 : 1);
     const int all = threads * (int)block.y;
-    const size_t smem = VEC > 1 ? (size_t)kQ8RowSlots * (g.r ? 2 : 1) * NV * 16 * all : 0;
+    const size_t smem = VEC > 1 ? (size_t)kQ8RowSlots * (RES ? 2 : 1) * NV * 16 * all : 0;
     if (smem > 40 * 1024) {  // more than a kernel has without asking, static part included
         static std::atomic<bool> ready[kMaxDevices];
-        const cudaError_t e = allow_smem(sv_q8_rows<ESZ, VEC, NV, MAXT>, kQ8RowsSmemMax, ready);
+        const cudaError_t e = allow_smem(sv_q8_rows<ESZ, VEC, NV, MAXT, RES>, kQ8RowsSmemMax, ready);
         if (e != cudaSuccess) return e;
     }
     // as many CTAs as are resident at once, each walking rows
@@ -58,15 +58,21 @@ cudaError_t q8_rows_go(const Q8RowsArgs& g, int threads, cudaStream_t st)
     int nreg = regs.load(std::memory_order_relaxed);
     if (!nreg) {
         cudaFuncAttributes a;
-        const cudaError_t e = cudaFuncGetAttributes(&a, sv_q8_rows<ESZ, VEC, NV, MAXT>);
+        const cudaError_t e = cudaFuncGetAttributes(&a, sv_q8_rows<ESZ, VEC, NV, MAXT, RES>);
         if (e != cudaSuccess) return e;
         nreg = (a.numRegs + 7) / 8 * 8;
         regs.store(nreg, std::memory_order_relaxed);
     }
     const long long fit = std::min<long long>(std::min(2048 / all, 65536 / (nreg * all)), (long long)(226 * 1024 / (smem + 2048)));
     const long long grid = std::min<long long>(cdiv(g.M, block.y), device_sm_count() * std::max<long long>(1, fit));
-    sv_q8_rows<ESZ, VEC, NV, MAXT><<<(unsigned)grid, block, smem, st>>>(g);
+    sv_q8_rows<ESZ, VEC, NV, MAXT, RES><<<(unsigned)grid, block, smem, st>>>(g);
     return cudaGetLastError();
+}
+
+template <int ESZ, int VEC, int NV, int MAXT>
+cudaError_t q8_rows_go(const Q8RowsArgs& g, int threads, cudaStream_t st)
+{
+    return g.r ? q8_rows_res<ESZ, VEC, NV, MAXT, true>(g, threads, st) : q8_rows_res<ESZ, VEC, NV, MAXT, false>(g, threads, st);
 }
 
 // A row by one warp, without barriers, where 4 pieces a thread (16 where the rows are

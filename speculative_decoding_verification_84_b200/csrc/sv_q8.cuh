@@ -6,9 +6,8 @@
 // even), scale = a / (127 rms), rms = sqrt(mean(s^2) + eps).  The norm's factor
 // cancels out of q, so one reduction gives everything: sum s^2 and max |p|.  Sums
 // are fp32 (fp64 where they leave its range), q is the integer that the formula
-// gives in fp64: fp32 decides all values but those within 6e-5 of a half (seven
-// roundings at most, 7 * 2^-24 * 127 = 5.3e-5), and those are decided in fp64,
-// against the fp64 maximum.
+// gives in fp64: fp32 decides all values but those that its roundings leave within
+// reach of a half, and those are decided in fp64, against the fp64 maximum.
 //   sv_q8_rows       a row in registers, blockDim.x threads a row
 //   sv_q8_rows_long  rows beyond that: read three times, fp64 throughout
 //
@@ -133,6 +132,8 @@ __global__ void __launch_bounds__(1024) sv_q8_rows_long(Q8RowsArgs g)
     }
 }
 
+__device__ __forceinline__ int cdiv_pos(int a, int b) { return a > 0 ? (a + b - 1) / b : 0; }
+
 __device__ __forceinline__ void q8_cp16(uint32_t dst, const void* src)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -156,6 +157,123 @@ __device__ __forceinline__ void q8_pairs(const uint4& v, unsigned long long (&p)
     for (int e = 0; e < P; ++e) p[e] = pack2(x[2 * e], x[2 * e + 1]);
 }
 
+// One row's elements in fp64: element e of piece j of the row's thread t, from shared
+// memory (VEC > 1) or global.
+template <int ESZ, int VEC, int NV, bool RES>
+struct Q8Row {
+    const Q8RowsArgs& g;
+    const uint4* slot;  // [x, r][NV][all], at the row's first thread
+    int all, row;
+    __device__ __forceinline__ int index(int j, int t) const { return (j * (int)blockDim.x + t) * VEC; }
+    __device__ __forceinline__ double sum(int j, int t, int e) const
+    {
+        if (VEC > 1) {
+            const uint4* at = slot + j * all + t;
+            const double x = q8_ld1<ESZ>(at, e);
+            return RES ? x + (double)q8_ld1<ESZ>(at + NV * all, e) : x;
+        }
+        const size_t i = (size_t)row * g.d + index(j, t);
+        const double x = q8_ld1<ESZ>(g.x, i);
+        return RES ? x + (double)q8_ld1<ESZ>(g.r, i) : x;
+    }
+    __device__ __forceinline__ double prod(int j, int t, int e) const
+    {
+        return sum(j, t, e) * (g.w ? (double)q8_ld1<ESZ>(g.w, index(j, t) + e) : 1.0);
+    }
+    // a piece's products in fp32, as the kernel forms them
+    __device__ __forceinline__ void products(int j, int t, float* p) const
+    {
+        if (VEC > 1) {
+            const uint4* at = slot + j * all + t;
+            const uint32_t one = ESZ == 2 ? 0x3f803f80u : 0x3f800000u;
+            float x[16 / ESZ], r[16 / ESZ], w[16 / ESZ];
+            unpack<ESZ>(at[0], x);
+            unpack<ESZ>(RES ? at[NV * all] : make_uint4(0, 0, 0, 0), r);
+            unpack<ESZ>(g.w ? __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(g.w) + (size_t)index(j, t) * ESZ))
+                            : make_uint4(one, one, one, one), w);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) p[e] = (RES ? x[e] + r[e] : x[e]) * w[e];
+        } else {
+            const size_t i = (size_t)row * g.d + index(j, t);
+            float s = q8_ld1<ESZ>(g.x, i);
+            if (RES) s += q8_ld1<ESZ>(g.r, i);
+            p[0] = s * (g.w ? q8_ld1<ESZ>(g.w, index(j, t)) : 1.f);
+        }
+    }
+};
+
+// The values of a warp's part of a row whose rounding fp32 leaves open, decided exactly
+// and written again: first 127 |p| against (n + 1/2) max with the fp32 maximum pmf,
+// good to 2^-23, which settles most; what that leaves open needs the fp64 maximum, unless
+// the products are exact in fp32.  That maximum lies among the values that reach the
+// fp32 one to 2^-20, in the parts of the row (s_pm, one a warp) that hold one.  Returns
+// the maximum as exactly as it was needed.  Out of line: about one warp in forty comes
+// here, and the kernel's registers are its occupancy.
+template <int ESZ, int VEC, int NV, bool RES>
+__device__ __noinline__ double q8_near(const Q8RowsArgs& g, const uint4* slot, int all, int row, float pmf, float k,
+                                       const unsigned* s_pm, bool near)
+{
+    const Q8Row<ESZ, VEC, NV, RES> in = {g, slot, all, row};
+    const int tid = threadIdx.x, lane = tid & 31, nw = blockDim.x >> 5;
+    const bool tiny = pmf < 0x1p-100f, exact = !tiny && !RES && (ESZ == 2 || !g.w);
+    int8_t* qrow = g.q + (size_t)row * g.ldq;
+    double dm = pmf;
+    unsigned todo = 0;  // elements j * VEC + e
+    if (near) {
+#pragma unroll 1
+        for (int j = 0; j < NV; ++j) {
+            if (in.index(j, tid) >= g.d) break;
+            float p[VEC];
+            in.products(j, tid, p);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const float t = p[e] * k;
+                if (tiny || fabsf(t - rintf(t)) > 0.5f - 0x1p-21f * fabsf(t)) todo |= 1u << (j * VEC + e);
+            }
+        }
+    }
+#pragma unroll 1
+    for (int round = 0; round < 2; ++round) {
+        unsigned open = 0;
+        for (unsigned left = todo; left; left &= left - 1) {
+            const int at = __ffs(left) - 1, j = at / VEC, e = at % VEC, i = in.index(j, tid) + e;
+            const double p = in.prod(j, tid, e);
+            if (round == 0 && !exact) {
+                const float n = floorf(fabsf((float)p) * k);  // |t| lies within 2^-21 |t| of n + 1/2
+                const double diff = fabs(p) * 127.0 - ((double)n + 0.5) * (double)pmf;
+                if (tiny || !(fabs(diff) > 0x1p-22 * ((double)n + 0.5) * (double)pmf)) {
+                    open |= 1u << at;
+                } else {
+                    const int m = (int)n + (diff > 0.0 ? 1 : 0);
+                    qrow[i] = (int8_t)(p < 0.0 ? -m : m);
+                }
+            } else {
+                qrow[i] = (int8_t)(int)(dm > 0.0 ? rint(p * 127.0 / dm) : 0.0);
+            }
+        }
+        todo = open;
+        if (round || !__any_sync(0xffffffffu, todo != 0u)) break;
+        const float thr = tiny ? 0.f : pmf * (1.f - 0x1p-20f);
+        dm = 0.0;
+        __syncwarp();  // one warp a row: the other lanes' copies
+        for (int t = 0; t < nw; ++t) {
+            if (nw > 1 && !(__uint_as_float(s_pm[t]) >= thr)) continue;
+#pragma unroll 1
+            for (int j = 0; j < NV; ++j) {
+                if (in.index(j, 32 * t + lane) >= g.d) break;
+                float p[VEC];
+                in.products(j, 32 * t + lane, p);
+                unsigned hit = 0;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) hit |= (fabsf(p[e]) >= thr ? 1u : 0u) << e;
+                for (; hit; hit &= hit - 1) dm = fmax(dm, fabs(in.prod(j, 32 * t + lane, __ffs(hit) - 1)));
+            }
+        }
+        dm = q8_warp_max(dm);
+    }
+    return dm;
+}
+
 constexpr int kQ8RowSlots = 3;
 
 // NV pieces of VEC elements a thread: 16-byte vectors, or (VEC = 1) elements, for rows
@@ -165,12 +283,11 @@ constexpr int kQ8RowSlots = 3;
 // Vectors come through shared memory by asynchronous copies, the next row's on the way
 // while this one is worked on (each thread copies what it reads itself, so no barrier
 // belongs to it).  The row's products stay in registers over the reduction, two
-// to an instruction throughout.  The fp64 maximum is formed only by a warp that holds
-// a value near a half, from the part of the row that holds the fp32 maximum, so the
-// row has one barrier; a warp can be one row ahead of another, hence three slots and
-// two sets of partials.  out_sum, which may be an input, is written last.
-template <int ESZ, int VEC, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NV <= 2 || (VEC == 1 && NV <= 8) ? 4 : 3) : 1) sv_q8_rows(Q8RowsArgs g)
+// to an instruction throughout.  A row has one barrier; a warp can be one row ahead of
+// another, hence three slots and two sets of partials.  out_sum may be an input: with
+// VEC = 1 it is written last, when no warp reads the row from memory any more.
+template <int ESZ, int VEC, int NV, int MAXT, bool RES>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NV <= 2 || (VEC == 1 && NV <= 8) ? 4 : 3) : 1) sv_q8_rows(const __grid_constant__ Q8RowsArgs g)
 {
     static_assert(VEC == 1 || VEC * ESZ == 16, "a piece is an element or a 16-byte vector");
     constexpr int P = VEC > 1 ? VEC / 2 : 1;   // packed pairs of a vector
@@ -179,69 +296,67 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NV <= 2 || (VEC == 1 && N
     __shared__ unsigned s_pm[2][32];
     __shared__ double s_sd[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x, nw = nthr >> 5;
-    const int all = nthr * blockDim.y, inputs = g.r ? 2 : 1;
+    constexpr int IN = RES ? 2 : 1;
+    const int all = nthr * blockDim.y;
     const int stride = gridDim.x * blockDim.y;
     const uint32_t one = ESZ == 2 ? 0x3f803f80u : 0x3f800000u;
     uint4* const slots = reinterpret_cast<uint4*>(q8_rows_dyn) + threadIdx.y * nthr;
+    const int mine = cdiv_pos(g.d - tid * VEC, nthr * VEC);  // pieces of a row that this thread has (at most NV)
 
-    auto copy = [&](int row, int slot) {
+    // to slot `slot`, from byte `from` of the inputs (this thread's first element of a row)
+    auto copy = [&](size_t from, int slot) {
         if (VEC == 1) return;
+        const uint32_t to = lr_smem(slots + slot * IN * NV * all + tid);
+        const char* x = static_cast<const char*>(g.x) + from;
+        const char* r = RES ? static_cast<const char*>(g.r) + from : nullptr;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int i = (j * nthr + tid) * VEC;
-            if (i < g.d) {
-                uint4* to = slots + (slot * inputs * NV + j) * all + tid;
-                q8_cp16(lr_smem(to), static_cast<const char*>(g.x) + ((size_t)row * g.d + i) * ESZ);
-                if (g.r) q8_cp16(lr_smem(to + NV * all), static_cast<const char*>(g.r) + ((size_t)row * g.d + i) * ESZ);
-            }
+            if (j >= mine) break;
+            q8_cp16(to + 16 * j * all, x + 16 * (size_t)(j * nthr));
+            if (RES) q8_cp16(to + 16 * (NV + j) * all, r + 16 * (size_t)(j * nthr));
         }
     };
+    // the weights, as packed as they came
+    uint4 wv[VEC > 1 ? NV : 1];
+    if (VEC > 1)
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            wv[j] = (g.w && j < mine) ? __ldg(reinterpret_cast<const uint4*>(g.w) + j * nthr + tid) : make_uint4(one, one, one, one);
     int row = blockIdx.x * blockDim.y + threadIdx.y, slot = 0, set = 0;
-    if (row < g.M) copy(row, 0);
+    size_t from = ((size_t)row * g.d + (size_t)tid * VEC) * ESZ;
+    const size_t from_step = (size_t)stride * g.d * ESZ;
+    if (row < g.M) copy(from, 0);
     asm volatile("cp.async.commit_group;" ::: "memory");
-    for (; row < g.M; row += stride, slot = slot == kQ8RowSlots - 1 ? 0 : slot + 1, set ^= 1) {
+    for (; row < g.M; row += stride, from += from_step, slot = slot == kQ8RowSlots - 1 ? 0 : slot + 1, set ^= 1) {
         const size_t base = (size_t)row * g.d;
-        // element e of piece j of thread t, in fp64: s, and s w
-        auto sum64 = [&](int j, int t, int e) {
-            const int i = (j * nthr + t) * VEC + e;
-            if (VEC > 1) {
-                const void* at = slots + (slot * inputs * NV + j) * all + t;
-                const double x = q8_ld1<ESZ>(at, e);
-                return g.r ? x + (double)q8_ld1<ESZ>(static_cast<const uint4*>(at) + NV * all, e) : x;
-            }
-            const double x = q8_ld1<ESZ>(g.x, base + i);
-            return g.r ? x + (double)q8_ld1<ESZ>(g.r, base + i) : x;
-        };
-        auto prod64 = [&](int j, int t, int e) {
-            return sum64(j, t, e) * (g.w ? (double)q8_ld1<ESZ>(g.w, (j * nthr + t) * VEC + e) : 1.0);
-        };
-        unsigned long long p2[VEC > 1 ? NV * P : 1], s2[VEC > 1 ? NV * P : 1];
-        uint32_t total[VEC > 1 && ESZ == 2 ? NV * P : 1];  // bf16: the sums as they are stored
+        const Q8Row<ESZ, VEC, NV, RES> in64 = {g, slots + slot * IN * NV * all, all, row};  // elements in fp64
+        unsigned long long p2[VEC > 1 ? NV * P : 1];
         float p1[VEC > 1 ? 1 : NV], s1[VEC > 1 ? 1 : NV];
         float tm = 0.f, ss;
         if (VEC > 1) {
-            if (row < g.M - stride) copy(row + stride, slot == kQ8RowSlots - 1 ? 0 : slot + 1);
+            if (row < g.M - stride) copy(from + from_step, slot == kQ8RowSlots - 1 ? 0 : slot + 1);
             asm volatile("cp.async.commit_group;" ::: "memory");
             asm volatile("cp.async.wait_group 1;" ::: "memory");
             unsigned long long acc[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
+            // (the weights stay packed from row to row: unpacked they take twice the registers)
+#pragma unroll
+            for (int j = 0; j < NV; ++j) asm volatile("" : "+r"(wv[j].x), "+r"(wv[j].y), "+r"(wv[j].z), "+r"(wv[j].w));
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const int i = (j * nthr + tid) * VEC;
-                uint4 x = make_uint4(0, 0, 0, 0), r = x, c = make_uint4(one, one, one, one);
-                if (i < g.d) {
-                    const uint4* at = slots + (slot * inputs * NV + j) * all + tid;
+                uint4 x = make_uint4(0, 0, 0, 0), r = x;
+                if (j < mine) {
+                    const uint4* at = slots + (slot * IN * NV + j) * all + tid;
                     x = *at;
-                    if (g.r) r = at[NV * all];
-                    if (g.w) c = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(g.w) + (size_t)i * ESZ));
+                    if (RES) r = at[NV * all];
                 }
                 unsigned long long a[P], b[P], w[P];
                 q8_pairs<ESZ>(x, a);
-                if (g.r) {
+                if (RES) {
                     q8_pairs<ESZ>(r, b);
 #pragma unroll
                     for (int e = 0; e < P; ++e) a[e] = add2(a[e], b[e]);
                 }
-                q8_pairs<ESZ>(c, w);
+                q8_pairs<ESZ>(wv[j], w);
 #pragma unroll
                 for (int e = 0; e < P; ++e) {
                     float u, v;
@@ -249,13 +364,12 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NV <= 2 || (VEC == 1 && N
                     p2[j * P + e] = mul2(a[e], w[e]);
                     unpack2(p2[j * P + e], u, v);
                     tm = q8_max3(tm, u, v);
-                    if (ESZ == 4) {
-                        s2[j * P + e] = a[e];
-                    } else {
-                        unpack2(a[e], u, v);
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(u, v);
-                        total[j * P + e] = *reinterpret_cast<const uint32_t*>(&h);
-                    }
+                }
+                if (g.sum && j < mine) {  // (may be written over x or r: they are in shared memory)
+                    float t[VEC];
+#pragma unroll
+                    for (int e = 0; e < P; ++e) unpack2(a[e], t[(2 * e) % VEC], t[(2 * e + 1) % VEC]);
+                    q8_st<ESZ, VEC>(g.sum, base + (size_t)(j * nthr + tid) * VEC, t);
                 }
             }
             float u, v;
@@ -268,7 +382,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NV <= 2 || (VEC == 1 && N
                 const int i = j * nthr + tid;
                 const bool in = i < g.d;
                 s1[j] = in ? q8_ld1<ESZ>(g.x, base + i) : 0.f;
-                if (in && g.r) s1[j] += q8_ld1<ESZ>(g.r, base + i);
+                if (in && RES) s1[j] += q8_ld1<ESZ>(g.r, base + i);
                 p1[j] = s1[j] * ((in && g.w) ? q8_ld1<ESZ>(g.w, i) : 1.f);
                 acc[j & 3] = fmaf(s1[j], s1[j], acc[j & 3]);
                 tm = q8_max3(tm, p1[j], 0.f);
@@ -305,7 +419,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NV <= 2 || (VEC == 1 && N
                 if ((j * nthr + tid) * VEC < g.d)
 #pragma unroll 1
                     for (int e = 0; e < VEC; ++e) {
-                        const double s = sum64(j, tid, e);
+                        const double s = in64.sum(j, tid, e);
                         sd += s * s;
                     }
             sd = q8_warp_sum(sd);
@@ -349,7 +463,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NV <= 2 || (VEC == 1 && N
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int i = (j * nthr + tid) * VEC;
-            if (i >= g.d) continue;
+            if (j >= mine) break;
             if (VEC == 1) {
                 qrow[i] = bad ? (int8_t)0 : (int8_t)o[j];
             } else if (VEC > 4) {
@@ -358,91 +472,18 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NV <= 2 || (VEC == 1 && N
                 *reinterpret_cast<uint32_t*>(qrow + i) = bad ? 0u : o[j * P / 2];
             }
         }
-        // values near a half: in fp64, and written again
-        const bool near = !bad && (tiny || far > 0.49994f);
-        double dm = pmf;  // the maximum, as exactly as it is needed
-        if (__any_sync(0xffffffffu, near)) {
-            unsigned todo = 0;  // elements j * VEC + e
-            if (near) {
-                unsigned long long K2 = pack2(k, k), magic = pack2(0x1.8p23f, 0x1.8p23f);
-#pragma unroll
-                for (int j = 0; j < NV; ++j)
-#pragma unroll
-                    for (int e = 0; e < VEC; e += 2) {
-                        float u = 0.f, v = 0.f;
-                        if (VEC > 1) {
-                            const unsigned long long t = mul2(p2[j * P + e / 2], K2);
-                            unpack2(sub2(t, sub2(add2(t, magic), magic)), u, v);
-                        } else {
-                            const float t = p1[j] * k;
-                            u = t - rintf(t);
-                        }
-                        if (tiny || fabsf(u) > 0.49994f) todo |= 1u << (j * VEC + e);
-                        if (VEC > 1 && (tiny || fabsf(v) > 0.49994f)) todo |= 2u << (j * VEC + e);
-                    }
-            }
-            // first against the fp32 maximum, good to 2^-23 (1.6e-5 of a value up to 127); what
-            // that leaves open needs the fp64 maximum, unless the products are exact in fp32
-            const bool exact = !tiny && !g.r && (ESZ == 2 || !g.w);
-            for (int round = 0; round < 2; ++round) {
-                unsigned open = 0;
-                for (unsigned left = todo; left; left &= left - 1) {
-                    const int at = __ffs(left) - 1, j = at / VEC, e = at % VEC, i = (j * nthr + tid) * VEC + e;
-                    if (i >= g.d) continue;
-                    const double t = dm > 0.0 ? prod64(j, tid, e) * 127.0 / dm : 0.0, n = rint(t);
-                    if (round == 0 && !exact && (tiny || fabs(t - n) > 0.49998)) open |= 1u << at;
-                    else qrow[i] = (int8_t)(int)n;
-                }
-                todo = open;
-                if (round || !__any_sync(0xffffffffu, todo != 0u)) break;
-                // the fp64 maximum: over the values that reach the fp32 one to 2^-20, in the
-                // parts of the row that hold one
-                const float thr = tiny ? 0.f : pmf * (1.f - 0x1p-20f);
-                dm = 0.0;
-                __syncwarp();  // one warp a row: the other lanes' copies
-                for (int t = 0; t < nw; ++t) {
-                    if (nw > 1 && !(__uint_as_float(s_pm[set][t]) >= thr)) continue;
-#pragma unroll 1
-                    for (int j = 0; j < NV; ++j) {
-                        const int i = (j * nthr + 32 * t + lane) * VEC;
-                        if (i >= g.d) continue;
-                        unsigned hit = 0;
-                        if (VEC > 1) {
-                            const uint4* at = slots + (slot * inputs * NV + j) * all + 32 * t + lane;
-                            const uint4 c = g.w ? __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(g.w) + (size_t)i * ESZ))
-                                                : make_uint4(one, one, one, one);
-                            float x[16 / ESZ], r[16 / ESZ], w[16 / ESZ];
-                            unpack<ESZ>(at[0], x);
-                            unpack<ESZ>(g.r ? at[NV * all] : make_uint4(0, 0, 0, 0), r);
-                            unpack<ESZ>(c, w);
-#pragma unroll
-                            for (int e = 0; e < VEC; ++e) hit |= (fabsf((x[e] + r[e]) * w[e]) >= thr ? 1u : 0u) << e;
-                        } else {
-                            hit = fabs(prod64(j, 32 * t + lane, 0)) >= (double)thr ? 1u : 0u;
-                        }
-                        for (; hit; hit &= hit - 1) dm = fmax(dm, fabs(prod64(j, 32 * t + lane, __ffs(hit) - 1)));
-                    }
-                }
-                dm = q8_warp_max(dm);
-            }
-        }
-        const double ms = !g.norm ? 1.0 : (again ? sd : (double)ss) / g.d + (double)g.eps;  // by all where g.normed, else by warp 0
-        if (tid == 0) g.scale[row] = bad ? NAN : (dm > 0.0 ? (float)(dm / (127.0 * sqrt(ms))) : 0.f);
-        float inv = 0.f;
-        bool wide = false;
+        double ms = 1.0;  // by all where g.normed, else by the first thread
+        if (g.norm && (tid == 0 || g.normed)) ms = (again ? sd : (double)ss) / g.d + (double)g.eps;
         if (g.normed) {
-            wide = !bad && (tiny || ms < 0x1p-200 || ms > 0x1p200);  // 1 / rms, or p, leaves fp32
-            inv = bad ? NAN : (ms > 0.0 ? (float)(1.0 / sqrt(ms)) : 0.f);
-        }
-        if (VEC == 1 && nw > 1 && g.sum) __syncthreads();  // another warp may still read inputs of this one's
+            const bool wide = !bad && (tiny || ms < 0x1p-200 || ms > 0x1p200);  // 1 / rms, or p, leaves fp32
+            const float inv = bad ? NAN : (ms > 0.0 ? (float)(1.0 / sqrt(ms)) : 0.f);
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int i = (j * nthr + tid) * VEC;
-            if (i >= g.d) continue;
-            if (g.normed) {
+            for (int j = 0; j < NV; ++j) {
+                const int i = (j * nthr + tid) * VEC;
+                if (j >= mine) break;
                 if (wide) {
 #pragma unroll 1
-                    for (int e = 0; e < VEC; ++e) q8_st1<ESZ>(g.normed, base + i + e, ms > 0.0 ? (float)(prod64(j, tid, e) / sqrt(ms)) : 0.f);
+                    for (int e = 0; e < VEC; ++e) q8_st1<ESZ>(g.normed, base + i + e, ms > 0.0 ? (float)(in64.prod(j, tid, e) / sqrt(ms)) : 0.f);
                 } else {
                     float y[VEC];
                     if (VEC > 1) {
@@ -456,20 +497,19 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NV <= 2 || (VEC == 1 && N
                     q8_st<ESZ, VEC>(g.normed, base + i, y);
                 }
             }
-            if (g.sum) {
-                if (VEC == 1) {
-                    q8_st1<ESZ>(g.sum, base + i, s1[j]);
-                } else if (ESZ == 2) {
-                    *reinterpret_cast<uint4*>(static_cast<char*>(g.sum) + (base + i) * ESZ) =
-                        make_uint4(total[(j * P) % (NV * P)], total[(j * P + 1) % (NV * P)], total[(j * P + 2) % (NV * P)],
-                                   total[(j * P + 3) % (NV * P)]);
-                } else {
-                    ulonglong2 t;
-                    t.x = s2[j * P];
-                    t.y = s2[j * P + P - 1];
-                    *reinterpret_cast<ulonglong2*>(static_cast<char*>(g.sum) + (base + i) * ESZ) = t;
-                }
-            }
+        }
+        // values whose rounding fp32 leaves open: seven roundings at most, so within
+        // 8 * 2^-24 |t| of a half
+        const bool near = !bad && (tiny || far > 0.5f - 0x1p-21f * tm * k);
+        double dm = pmf;  // the maximum, as exactly as it is needed
+        if (__any_sync(0xffffffffu, near))
+            dm = q8_near<ESZ, VEC, NV, RES>(g, slots + slot * IN * NV * all, all, row, pmf, k, s_pm[set], near);
+        if (tid == 0) g.scale[row] = bad ? NAN : (dm > 0.0 ? (float)(dm / (127.0 * sqrt(ms))) : 0.f);
+        if (VEC == 1 && g.sum) {
+            if (nw > 1) __syncthreads();  // another warp may still read inputs of this one's from memory
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (j < mine) q8_st1<ESZ>(g.sum, base + j * nthr + tid, s1[j]);
         }
     }
 }
