@@ -211,26 +211,49 @@ cudaError_t q8_gemm_launch(const void* a, long long lda, const void* w, long lon
     CUtensorMap tw, ta;
     if (!q8_map(&tw, w, g.V, g.K, ldw, kQ8BM) || !q8_map(&ta, a, g.M, g.K, lda, mine)) return cudaErrorInvalidValue;
     const long long tiles = (long long)g.m_tiles * g.v_tiles;
+    if (tiles + sms > 0x7fffffffLL || (long long)g.v_tiles * 2 * kQ8BM > 0x7fffffffLL || (long long)g.M + 1024 > 0x7fffffffLL)
+        return cudaErrorInvalidValue;
     const size_t smem = 1024 + (size_t)g.stages * g.sub * (kQ8WBytes + g.groups * mine * kQ8BK);
-    if (!pairs) {
-        static std::atomic<bool> ready[kMaxDevices];
-        if ((e = allow_smem(sv_q8_gemm<ESZ, false>, kQ8SmemMax, ready)) != cudaSuccess) return e;
-        sv_q8_gemm<ESZ, false><<<(unsigned)std::min<long long>(tiles, sms), kQ8Threads, smem, st>>>(tw, ta, g);
-        return cudaGetLastError();
-    }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(2 * std::min<long long>(tiles, resident)));
+    cfg.gridDim = dim3((unsigned)(pairs ? 2 * std::min<long long>(tiles, resident) : std::min<long long>(tiles, sms)));
     cfg.blockDim = dim3(kQ8Threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, sv_q8_gemm<ESZ, true>, tw, ta, g);
+    if (pairs) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[cfg.numAttrs].val.clusterDim.x = 2;
+        attr[cfg.numAttrs].val.clusterDim.y = 1;
+        attr[cfg.numAttrs++].val.clusterDim.z = 1;
+    }
+    if (g.overlap) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (pairs) return cudaLaunchKernelEx(&cfg, sv_q8_gemm<ESZ, true>, tw, ta, g);
+    static std::atomic<bool> ready[kMaxDevices];
+    if ((e = allow_smem(sv_q8_gemm<ESZ, false>, kQ8SmemMax, ready)) != cudaSuccess) return e;
+    return cudaLaunchKernelEx(&cfg, sv_q8_gemm<ESZ, false>, tw, ta, g);
+}
+
+// after_norm: the launch before this one on the stream is the norm of `a`, which the
+// product may overlap (its weights are older than that).
+sv_status q8_gemm(const int8_t* a, int lda, const float* a_scale, const int8_t* w, int ldw, const float* w_scale, int M, int K,
+                  int V, void* out, sv_dtype dt, int32_t* err, bool after_norm, cudaStream_t st)
+{
+    Q8GemmArgs g = {};
+    g.out = out;
+    g.a_scale = a_scale;
+    g.w_scale = w_scale;
+    g.err = err;
+    g.M = M;
+    g.V = V;
+    g.K = K;
+    g.overlap = after_norm ? 1 : 0;
+    const cudaError_t e = dt == SV_DTYPE_BF16 ? q8_gemm_launch<2>(a, lda, w, ldw, g, st)
+                                              : q8_gemm_launch<4>(a, lda, w, ldw, g, st);
+    return e == cudaSuccess ? SV_OK : (e == cudaErrorInvalidValue ? SV_ERR_INVALID_ARG : SV_ERR_CUDA);
 }
 
 sv_status q8_gemm_check(const void* a, int lda, const void* a_scale, const void* w, int ldw, const void* w_scale, int M,
@@ -344,17 +367,7 @@ extern "C" sv_status spec_verify_q8_matmul(const int8_t* a, int lda, const float
 {
     const sv_status s = q8_gemm_check(a, lda, a_scale, w, ldw, w_scale, M, K, V, out, dt, out_error);
     if (s != SV_OK) return s;
-    Q8GemmArgs g = {};
-    g.out = out;
-    g.a_scale = a_scale;
-    g.w_scale = w_scale;
-    g.err = out_error;
-    g.M = M;
-    g.V = V;
-    g.K = K;
-    const cudaError_t e = dt == SV_DTYPE_BF16 ? q8_gemm_launch<2>(a, lda, w, ldw, g, (cudaStream_t)stream)
-                                              : q8_gemm_launch<4>(a, lda, w, ldw, g, (cudaStream_t)stream);
-    return e == cudaSuccess ? SV_OK : (e == cudaErrorInvalidValue ? SV_ERR_INVALID_ARG : SV_ERR_CUDA);
+    return q8_gemm(a, lda, a_scale, w, ldw, w_scale, M, K, V, out, dt, out_error, false, (cudaStream_t)stream);
 }
 
 extern "C" size_t spec_verify_q8_head_workspace_size(int M, int d)
@@ -381,7 +394,7 @@ extern "C" sv_status spec_verify_q8_head(const void* x, const void* residual, co
     if (s != SV_OK) return s;
     s = spec_verify_q8_norm(x, residual, weight, dt, eps, M, d, q, ld, scale, out_sum, nullptr, stream);
     if (s != SV_OK) return s;
-    return spec_verify_q8_matmul(q, ld, scale, w, ldw, w_scale, M, d, V, out_logits, out_dt, out_error, stream);
+    return q8_gemm(q, ld, scale, w, ldw, w_scale, M, d, V, out_logits, out_dt, out_error, true, (cudaStream_t)stream);
 }
 
 extern "C" size_t spec_verify_beam_workspace_size(int B, int W, int V, int K, sv_dtype dt)

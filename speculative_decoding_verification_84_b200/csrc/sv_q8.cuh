@@ -296,6 +296,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NV <= 2 || (VEC == 1 && N
     __shared__ unsigned s_pm[2][32];
     __shared__ double s_sd[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x, nw = nthr >> 5;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product may load its weights
     constexpr int IN = RES ? 2 : 1;
     const int all = nthr * blockDim.y;
     const int stride = gridDim.x * blockDim.y;
@@ -539,6 +540,7 @@ struct Q8GemmArgs {
     int buf_cols, tmem_cols;
     int m_tiles, v_tiles;
     int stages, sub;       // of `sub` K blocks each
+    int overlap;           // a programmatic dependent of the kernel that writes a and a_scale
 };
 
 // Instruction descriptor: s32 accumulator, signed 8-bit A and B, both K-major, m x n.
@@ -729,8 +731,8 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     const int kbs = (g.K + kQ8BK - 1) / kQ8BK, S = g.stages, G = g.groups;
     const int mine = g.nt / CTAS, a_bytes = mine * kQ8BK;  // this CTA's tokens of an accumulator
     const int BLOCK = kQ8WBytes + G * a_bytes, SUB = g.sub, STAGE = SUB * BLOCK;
-    const long long tiles = (long long)g.m_tiles * g.v_tiles;
-    const long long first = blockIdx.x / CTAS, step = gridDim.x / CTAS;
+    const unsigned tiles = (unsigned)g.m_tiles * (unsigned)g.v_tiles, m_tiles = (unsigned)g.m_tiles;  // fits an int
+    const unsigned first = blockIdx.x / CTAS, step = gridDim.x / CTAS;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -768,26 +770,57 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         int it = 0;
         bool ok = true;
         const uint32_t bars = q8_leader<PAIR>(full);
-        for (long long t = first; ok && t < tiles; t += step) {
-            const int m0 = (int)(t % g.m_tiles) * G * g.nt + rank * mine;
-            const int v0 = ((int)(t / g.m_tiles) * CTAS + rank) * kQ8BM;
-            for (int kb = 0; kb < kbs; kb += SUB) {
-                if (it >= S && !q8_wait(&empty[r.s], r.phase ^ 1u, abort, g.err)) { ok = false; break; }
-                if (q8_elect()) {
-                    unsigned char* st = ring + r.s * STAGE;
-                    const uint32_t bar = bars + 8u * r.s;
-                    const int subs = min(SUB, kbs - kb);
-                    if (rank == 0) lr_expect_tx(&full[r.s], (unsigned)(CTAS * subs * BLOCK));
-                    for (int u = 0; u < subs; ++u, st += BLOCK) {
-                        q8_tma<PAIR>(st, &tw, bar, (kb + u) * kQ8BK, v0);
-                        q8_tma<PAIR>(st + kQ8WBytes, &ta, bar, (kb + u) * kQ8BK, m0);
-                        if (G > 1) q8_tma<PAIR>(st + kQ8WBytes + a_bytes, &ta, bar, (kb + u) * kQ8BK, m0 + g.nt);
-                    }
-                }
-                __syncwarp();
-                ++it;
-                r.next(S);
+        // a place among the stages to load: K block kb of tile t, whose rows start at m0 and v0
+        struct Place {
+            unsigned t;
+            int kb, m0, v0;
+        };
+        auto tile = [&](Place& p) {
+            p.kb = 0;
+            const unsigned v = p.t / m_tiles;
+            p.m0 = (int)(p.t - v * m_tiles) * G * g.nt + rank * mine;
+            p.v0 = ((int)v * CTAS + rank) * kQ8BM;
+        };
+        auto next = [&](Place& p) {
+            if ((p.kb += SUB) >= kbs) {
+                p.t += step;
+                tile(p);
             }
+        };
+        // the weights' and / or the tokens' copies of a stage, into place s of the ring
+        auto issue = [&](const Place& p, int s, bool weights, bool tokens) {
+            if (q8_elect()) {
+                unsigned char* st = ring + s * STAGE;
+                const uint32_t bar = bars + 8u * s;
+                const int subs = min(SUB, kbs - p.kb);
+                if (weights && rank == 0) lr_expect_tx(&full[s], (unsigned)(CTAS * subs * BLOCK));
+                for (int u = 0; u < subs; ++u, st += BLOCK) {
+                    const int x = (p.kb + u) * kQ8BK;
+                    if (weights) q8_tma<PAIR>(st, &tw, bar, x, p.v0);
+                    if (tokens) q8_tma<PAIR>(st + kQ8WBytes, &ta, bar, x, p.m0);
+                    if (tokens && G > 1) q8_tma<PAIR>(st + kQ8WBytes + a_bytes, &ta, bar, x, p.m0 + g.nt);
+                }
+            }
+            __syncwarp();
+        };
+        // the first round of the ring; where the kernel before is the norm of the tokens, the
+        // weights do not wait for it
+        Place p = {first, 0, 0, 0};
+        tile(p);
+        Place p0 = p;
+        if (g.overlap) {
+            for (; it < S && p.t < tiles; ++it, next(p)) issue(p, it, true, false);
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            for (int u = 0; u < it; ++u, next(p0)) issue(p0, u, false, true);
+        } else {
+            for (; it < S && p.t < tiles; ++it, next(p)) issue(p, it, true, true);
+        }
+        if (it == S) r.phase = 1u;
+        for (; p.t < tiles; ++it, next(p)) {
+            ok = q8_wait(&empty[r.s], r.phase ^ 1u, abort, g.err);
+            if (!ok) break;
+            issue(p, r.s, true, true);
+            r.next(S);
         }
         // every stage handed back: nothing of the pair's is still on its way to this CTA
         for (int u = max(0, it - S); ok && u < it; ++u) ok = q8_wait(&empty[u % S], (unsigned)(u / S) & 1u, abort, g.err);
@@ -798,7 +831,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         Q8Ring r, acc;
         int used = 0;  // accumulators so far, up to g.bufs
         bool ok = true;
-        for (long long t = first; ok && t < tiles; t += step) {
+        for (unsigned t = first; ok && t < tiles; t += step) {
             uint32_t d[2];
             int buf[2];
             for (int h = 0; h < G; ++h) {
@@ -840,9 +873,11 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         const int q = (warp - 4) & 3, grp = (warp - 4) >> 2;
         Q8Ring acc;
         bool ok = true;
-        for (long long t = first; ok && t < tiles; t += step) {
-            const int m0 = (int)(t % g.m_tiles) * G * g.nt;
-            const int v = ((int)(t / g.m_tiles) * CTAS + rank) * kQ8BM + 32 * q + lane;
+        asm volatile("griddepcontrol.wait;" ::: "memory");  // the tokens' scales
+        for (unsigned t = first; ok && t < tiles; t += step) {
+            const unsigned vt = t / m_tiles;
+            const int m0 = (int)(t - vt * m_tiles) * G * g.nt;
+            const int v = ((int)vt * CTAS + rank) * kQ8BM + 32 * q + lane;
             for (int h = 0; h < G; ++h) {
                 // the warp-wide tcgen05.ld below runs on all lanes or none
                 ok = q8_wait(&tfull[acc.s], acc.phase, abort, g.err);
