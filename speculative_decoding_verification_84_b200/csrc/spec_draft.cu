@@ -39,18 +39,23 @@ cudaError_t allow_smem(Kernel kernel, int bytes, std::atomic<bool> (&ready)[kMax
 
 // ----------------------------------------------------------------------------- rows to int8
 
-constexpr int kQ8RowsSmemMax = 200 * 1024;  // three rows of x and of the residual
+constexpr int kQ8RowsSmemMax = 208 * 1024;
 
-template <int ESZ, int VEC, int NV, int MAXT, bool RES>
-cudaError_t q8_rows_res(const Q8RowsArgs& g, int threads, cudaStream_t st)
+size_t q8_rows_smem(int nv, int threads, int rows, bool res, bool al)
+{
+    return (size_t)16 * q8_rows_kept(res, al) * rows * q8_row_blocks(nv, threads);
+}
+
+template <int ESZ, int NV, int MAXT, bool RES, bool AL>
+cudaError_t q8_rows_go(const Q8RowsArgs& g, int threads, cudaStream_t st)
 {
     // rows of one warp: eight to a CTA
     const dim3 block(threads, threads == 32 ? 8 : 1);
     const int all = threads * (int)block.y;
-    const size_t smem = VEC > 1 ? (size_t)kQ8RowSlots * (RES ? 2 : 1) * NV * 16 * all : 0;
+    const size_t smem = q8_rows_smem(NV, threads, (int)block.y, RES, AL);
     if (smem > 40 * 1024) {  // more than a kernel has without asking, static part included
         static std::atomic<bool> ready[kMaxDevices];
-        const cudaError_t e = allow_smem(sv_q8_rows<ESZ, VEC, NV, MAXT, RES>, kQ8RowsSmemMax, ready);
+        const cudaError_t e = allow_smem(sv_q8_rows<ESZ, NV, MAXT, RES, AL>, kQ8RowsSmemMax, ready);
         if (e != cudaSuccess) return e;
     }
     // as many CTAs as are resident at once, each walking rows
@@ -58,50 +63,48 @@ cudaError_t q8_rows_res(const Q8RowsArgs& g, int threads, cudaStream_t st)
     int nreg = regs.load(std::memory_order_relaxed);
     if (!nreg) {
         cudaFuncAttributes a;
-        const cudaError_t e = cudaFuncGetAttributes(&a, sv_q8_rows<ESZ, VEC, NV, MAXT, RES>);
+        const cudaError_t e = cudaFuncGetAttributes(&a, sv_q8_rows<ESZ, NV, MAXT, RES, AL>);
         if (e != cudaSuccess) return e;
         nreg = (a.numRegs + 7) / 8 * 8;
         regs.store(nreg, std::memory_order_relaxed);
     }
     const long long fit = std::min<long long>(std::min(2048 / all, 65536 / (nreg * all)), (long long)(226 * 1024 / (smem + 2048)));
     const long long grid = std::min<long long>(cdiv(g.M, block.y), device_sm_count() * std::max<long long>(1, fit));
-    sv_q8_rows<ESZ, VEC, NV, MAXT, RES><<<(unsigned)grid, block, smem, st>>>(g);
+    sv_q8_rows<ESZ, NV, MAXT, RES, AL><<<(unsigned)grid, block, smem, st>>>(g);
     return cudaGetLastError();
 }
 
-template <int ESZ, int VEC, int NV, int MAXT>
-cudaError_t q8_rows_go(const Q8RowsArgs& g, int threads, cudaStream_t st)
-{
-    return g.r ? q8_rows_res<ESZ, VEC, NV, MAXT, true>(g, threads, st) : q8_rows_res<ESZ, VEC, NV, MAXT, false>(g, threads, st);
-}
-
-// A row by one warp, without barriers, where 4 pieces a thread (16 where the rows are
-// not 16-byte multiples and a piece is an element) are enough, else by up to 256 threads
-// with as few pieces each as that allows, else by up to 1024; beyond that from memory,
-// three times.
-template <int ESZ, int VEC>
+// A row by one warp, without barriers across warps, where 4 vectors a thread are enough,
+// else by up to 256 threads with as few vectors each as that allows, else by up to 1024;
+// rows that shared memory cannot hold three of, from memory, three times.
+template <int ESZ, bool RES, bool AL>
 cudaError_t q8_rows_launch(const Q8RowsArgs& g, cudaStream_t st)
 {
-    constexpr int N1 = VEC > 1 ? 1 : 4, N2 = VEC > 1 ? 2 : 8, N3 = VEC > 1 ? 4 : 16;
-    const long long pieces = cdiv(g.d, VEC);
-    const int room = pieces <= 32 * N3 ? 32 : 256;
-    const int nv = cdiv(pieces, N1) <= room ? N1 : (cdiv(pieces, N2) <= room ? N2 : N3);
+    const long long pieces = cdiv((long long)g.d * ESZ, 16);
+    const int room = pieces <= 32 * 4 ? 32 : 256;
+    const int nv = pieces <= room ? 1 : (pieces <= 2 * room ? 2 : 4);
     const long long threads = cdiv(cdiv(pieces, nv), 32) * 32;
-    if (threads > 1024 || (VEC > 1 && (long long)kQ8RowSlots * (g.r ? 2 : 1) * nv * 16 * threads > kQ8RowsSmemMax)) {
+    if (threads > 1024 || q8_rows_smem(nv, (int)threads, threads == 32 ? 8 : 1, RES, AL) > (size_t)kQ8RowsSmemMax) {
         sv_q8_rows_long<ESZ><<<(unsigned)g.M, 1024, 0, st>>>(g);
         return cudaGetLastError();
     }
-    if (threads > 256) return q8_rows_go<ESZ, VEC, N3, 1024>(g, (int)threads, st);
-    if (nv == N1) return q8_rows_go<ESZ, VEC, N1, 256>(g, (int)threads, st);
-    if (nv == N2) return q8_rows_go<ESZ, VEC, N2, 256>(g, (int)threads, st);
-    return q8_rows_go<ESZ, VEC, N3, 256>(g, (int)threads, st);
+    if (threads > 256) return q8_rows_go<ESZ, 4, 1024, RES, AL>(g, (int)threads, st);
+    if (nv == 1) return q8_rows_go<ESZ, 1, 256, RES, AL>(g, (int)threads, st);
+    if (nv == 2) return q8_rows_go<ESZ, 2, 256, RES, AL>(g, (int)threads, st);
+    return q8_rows_go<ESZ, 4, 256, RES, AL>(g, (int)threads, st);
+}
+
+template <int ESZ>
+cudaError_t q8_rows_dt(const Q8RowsArgs& g, cudaStream_t st)
+{
+    const bool al = (long long)g.d * ESZ % 16 == 0;  // every row on a 16-byte boundary
+    if (g.r) return al ? q8_rows_launch<ESZ, true, true>(g, st) : q8_rows_launch<ESZ, true, false>(g, st);
+    return al ? q8_rows_launch<ESZ, false, true>(g, st) : q8_rows_launch<ESZ, false, false>(g, st);
 }
 
 sv_status q8_rows(const Q8RowsArgs& g, sv_dtype dt, cudaStream_t st)
 {
-    const bool bf = dt == SV_DTYPE_BF16, vec = (long long)g.d * (bf ? 2 : 4) % 16 == 0;
-    const cudaError_t e = bf ? (vec ? q8_rows_launch<2, 8>(g, st) : q8_rows_launch<2, 1>(g, st))
-                             : (vec ? q8_rows_launch<4, 4>(g, st) : q8_rows_launch<4, 1>(g, st));
+    const cudaError_t e = dt == SV_DTYPE_BF16 ? q8_rows_dt<2>(g, st) : q8_rows_dt<4>(g, st);
     return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 

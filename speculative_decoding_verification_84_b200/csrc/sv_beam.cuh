@@ -20,7 +20,7 @@
 //                  binary search.  A programmatic dependent of sv_beam_rows.
 // Selecting inside the pass (each CTA its segment's K best, with group maxima for
 // a threshold) cost more than the pass: 64 x 8 x 128256 bf16, K = 8, took 49 us in
-// that form against BEAM_ROWS_US.
+// that form against 27 us for the pass and 12 for the pick.
 // Batches are cut by token index, so equal rows give equal normalisers wherever
 // they lie in memory.
 //
@@ -102,17 +102,6 @@ __device__ __noinline__ uint4 beam_ld_edge(const unsigned char* p, int i, int V)
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// 16 bytes starting `sh` bytes into the 32 of (lo, hi); sh is one value for the row.
-__device__ __forceinline__ uint4 beam_shift(const uint4& lo, const uint4& hi, unsigned sh)
-{
-    uint32_t w0 = lo.x, w1 = lo.y, w2 = lo.z, w3 = lo.w, w4 = hi.x, w5 = hi.y;
-    if (sh & 8u) { w0 = lo.z; w1 = lo.w; w2 = hi.x; w3 = hi.y; w4 = hi.z; w5 = hi.w; }
-    if (sh & 4u) { w0 = w1; w1 = w2; w2 = w3; w3 = w4; w4 = w5; }
-    const unsigned b = (sh & 3u) * 8u;
-    return make_uint4(__funnelshift_r(w0, w1, b), __funnelshift_r(w1, w2, b), __funnelshift_r(w2, w3, b),
-                      __funnelshift_r(w3, w4, b));
-}
-
 // Row elements [i, i + VEC), -inf past V, of a row that may start off a 16-byte
 // boundary: only blocks that hold an element of the row are read, and no byte past `end`.
 template <int ESZ, bool AL>
@@ -125,7 +114,7 @@ __device__ __forceinline__ uint4 beam_ld(const unsigned char* row, int i, int V,
     const unsigned sh = (unsigned)(reinterpret_cast<uintptr_t>(row) & 15u);
     const unsigned char* a = p - sh;
     if (i + 16 / ESZ <= V && a + 32 <= end)
-        return beam_shift(__ldg(reinterpret_cast<const uint4*>(a)), __ldg(reinterpret_cast<const uint4*>(a) + 1), sh);
+        return shift16(__ldg(reinterpret_cast<const uint4*>(a)), __ldg(reinterpret_cast<const uint4*>(a) + 1), sh);
     return beam_ld_edge<ESZ>(p, i, V);
 }
 
@@ -250,7 +239,7 @@ __global__ void __launch_bounds__(kBeamThreads, 3) sv_beam_rows(BeamArgs g, int 
                 __syncwarp();  // the other lanes' copies
                 const unsigned sh = (unsigned)(reinterpret_cast<uintptr_t>(base + (size_t)row * g.V * ESZ) & 15u);
 #pragma unroll
-                for (int j = 0; j < NV; ++j) v[j] = beam_shift(at[j * 32], at[j * 32 + 1], sh);
+                for (int j = 0; j < NV; ++j) v[j] = shift16(at[j * 32], at[j * 32 + 1], sh);
                 if ((batch + 1) * STEP > g.V) {  // elements past the row
 #pragma unroll
                     for (int j = 0; j < NV; ++j) {

@@ -127,6 +127,17 @@ __device__ __forceinline__ float vec_max(const uint4& v)
     }
 }
 
+// 16 bytes starting `sh` bytes into the 32 of (lo, hi); sh is one value for a row.
+__device__ __forceinline__ uint4 shift16(const uint4& lo, const uint4& hi, unsigned sh)
+{
+    uint32_t w0 = lo.x, w1 = lo.y, w2 = lo.z, w3 = lo.w, w4 = hi.x, w5 = hi.y;
+    if (sh & 8u) { w0 = lo.z; w1 = lo.w; w2 = hi.x; w3 = hi.y; w4 = hi.z; w5 = hi.w; }
+    if (sh & 4u) { w0 = w1; w1 = w2; w2 = w3; w3 = w4; w4 = w5; }
+    const unsigned b = (sh & 3u) * 8u;
+    return make_uint4(__funnelshift_r(w0, w1, b), __funnelshift_r(w1, w2, b), __funnelshift_r(w2, w3, b),
+                      __funnelshift_r(w3, w4, b));
+}
+
 // ---- online log-sum-exp state with integer offsets
 struct Lse {
     float m, mk, s;

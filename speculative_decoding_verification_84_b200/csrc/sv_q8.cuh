@@ -58,23 +58,18 @@ __device__ __forceinline__ void q8_st1(void* p, size_t i, float v)
     else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
 }
 
-// VEC elements (16 bytes, or one)
-template <int ESZ, int VEC>
-__device__ __forceinline__ void q8_st(void* p, size_t i, const float* v)
+// 16 / ESZ values rounded and packed into 16 bytes.
+template <int ESZ>
+__device__ __forceinline__ uint4 q8_pack(const float* v)
 {
-    if (VEC == 1) {
-        q8_st1<ESZ>(p, i, v[0]);
-    } else if (ESZ == 2) {
-        uint32_t o[4];
+    if (ESZ == 4) return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    uint32_t o[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v[(2 * e) % VEC], v[(2 * e + 1) % VEC]);
-            o[e] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        *reinterpret_cast<uint4*>(static_cast<char*>(p) + i * ESZ) = make_uint4(o[0], o[1], o[2], o[3]);
-    } else {
-        *reinterpret_cast<float4*>(static_cast<char*>(p) + i * ESZ) = make_float4(v[0], v[1 % VEC], v[2 % VEC], v[3 % VEC]);
+    for (int e = 0; e < 4; ++e) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[(2 * e) % (16 / ESZ)], v[(2 * e + 1) % (16 / ESZ)]);
+        o[e] = *reinterpret_cast<const uint32_t*>(&h);
     }
+    return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 __device__ __forceinline__ double q8_warp_sum(double v)
@@ -134,9 +129,10 @@ __global__ void __launch_bounds__(1024) sv_q8_rows_long(Q8RowsArgs g)
 
 __device__ __forceinline__ int cdiv_pos(int a, int b) { return a > 0 ? (a + b - 1) / b : 0; }
 
-__device__ __forceinline__ void q8_cp16(uint32_t dst, const void* src)
+// 16 bytes of shared memory, of which `bytes` are read and the rest are zero.
+__device__ __forceinline__ void q8_cp16(uint32_t dst, const void* src, int bytes)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
 // max(m, |a|, |b|); a NaN stays
@@ -157,47 +153,42 @@ __device__ __forceinline__ void q8_pairs(const uint4& v, unsigned long long (&p)
     for (int e = 0; e < P; ++e) p[e] = pack2(x[2 * e], x[2 * e + 1]);
 }
 
-// One row's elements in fp64: element e of piece j of the row's thread t, from shared
-// memory (VEC > 1) or global.
-template <int ESZ, int VEC, int NV, bool RES>
+// A row in shared memory: element e of piece j of the row's thread t, in fp64.
+template <int ESZ, bool RES, bool AL>
 struct Q8Row {
+    static constexpr int VEC = 16 / ESZ;
     const Q8RowsArgs& g;
-    const uint4* slot;  // [x, r][NV][all], at the row's first thread
-    int all, row;
+    const unsigned char* x;  // the row's first element
+    int residual;            // bytes from there to the residual's
     __device__ __forceinline__ int index(int j, int t) const { return (j * (int)blockDim.x + t) * VEC; }
-    __device__ __forceinline__ double sum(int j, int t, int e) const
+    __device__ __forceinline__ double sum(int i) const
     {
-        if (VEC > 1) {
-            const uint4* at = slot + j * all + t;
-            const double x = q8_ld1<ESZ>(at, e);
-            return RES ? x + (double)q8_ld1<ESZ>(at + NV * all, e) : x;
-        }
-        const size_t i = (size_t)row * g.d + index(j, t);
-        const double x = q8_ld1<ESZ>(g.x, i);
-        return RES ? x + (double)q8_ld1<ESZ>(g.r, i) : x;
+        const double v = q8_ld1<ESZ>(x, i);
+        return RES ? v + (double)q8_ld1<ESZ>(x + residual, i) : v;
     }
-    __device__ __forceinline__ double prod(int j, int t, int e) const
+    __device__ __forceinline__ double prod(int i) const { return sum(i) * (g.w ? (double)q8_ld1<ESZ>(g.w, i) : 1.0); }
+    // elements i .. i + VEC in fp32, the products as the kernel forms them; 0 past the row
+    __device__ __forceinline__ void products(int i, float* p) const
     {
-        return sum(j, t, e) * (g.w ? (double)q8_ld1<ESZ>(g.w, index(j, t) + e) : 1.0);
-    }
-    // a piece's products in fp32, as the kernel forms them
-    __device__ __forceinline__ void products(int j, int t, float* p) const
-    {
-        if (VEC > 1) {
-            const uint4* at = slot + j * all + t;
+        if (AL) {
             const uint32_t one = ESZ == 2 ? 0x3f803f80u : 0x3f800000u;
-            float x[16 / ESZ], r[16 / ESZ], w[16 / ESZ];
-            unpack<ESZ>(at[0], x);
-            unpack<ESZ>(RES ? at[NV * all] : make_uint4(0, 0, 0, 0), r);
-            unpack<ESZ>(g.w ? __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(g.w) + (size_t)index(j, t) * ESZ))
+            float s[VEC], r[VEC], w[VEC];
+            unpack<ESZ>(*reinterpret_cast<const uint4*>(x + i * ESZ), s);
+            unpack<ESZ>(RES ? *reinterpret_cast<const uint4*>(x + residual + i * ESZ) : make_uint4(0, 0, 0, 0), r);
+            unpack<ESZ>(g.w ? __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(g.w) + (size_t)i * ESZ))
                             : make_uint4(one, one, one, one), w);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) p[e] = (RES ? x[e] + r[e] : x[e]) * w[e];
+            for (int e = 0; e < VEC; ++e) p[e] = (RES ? s[e] + r[e] : s[e]) * w[e];
         } else {
-            const size_t i = (size_t)row * g.d + index(j, t);
-            float s = q8_ld1<ESZ>(g.x, i);
-            if (RES) s += q8_ld1<ESZ>(g.r, i);
-            p[0] = s * (g.w ? q8_ld1<ESZ>(g.w, index(j, t)) : 1.f);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                p[e] = 0.f;
+                if (i + e < g.d) {
+                    float s = q8_ld1<ESZ>(x, i + e);
+                    if (RES) s += q8_ld1<ESZ>(x + residual, i + e);
+                    p[e] = s * (g.w ? q8_ld1<ESZ>(g.w, i + e) : 1.f);
+                }
+            }
         }
     }
 };
@@ -209,11 +200,12 @@ struct Q8Row {
 // fp32 one to 2^-20, in the parts of the row (s_pm, one a warp) that hold one.  Returns
 // the maximum as exactly as it was needed.  Out of line: about one warp in forty comes
 // here, and the kernel's registers are its occupancy.
-template <int ESZ, int VEC, int NV, bool RES>
-__device__ __noinline__ double q8_near(const Q8RowsArgs& g, const uint4* slot, int all, int row, float pmf, float k,
+template <int ESZ, int NV, bool RES, bool AL>
+__device__ __noinline__ double q8_near(const Q8RowsArgs& g, const unsigned char* x, int residual, int row, float pmf, float k,
                                        const unsigned* s_pm, bool near)
 {
-    const Q8Row<ESZ, VEC, NV, RES> in = {g, slot, all, row};
+    constexpr int VEC = 16 / ESZ;
+    const Q8Row<ESZ, RES, AL> in = {g, x, residual};
     const int tid = threadIdx.x, lane = tid & 31, nw = blockDim.x >> 5;
     const bool tiny = pmf < 0x1p-100f, exact = !tiny && !RES && (ESZ == 2 || !g.w);
     int8_t* qrow = g.q + (size_t)row * g.ldq;
@@ -222,13 +214,14 @@ __device__ __noinline__ double q8_near(const Q8RowsArgs& g, const uint4* slot, i
     if (near) {
 #pragma unroll 1
         for (int j = 0; j < NV; ++j) {
-            if (in.index(j, tid) >= g.d) break;
+            const int i = in.index(j, tid);
+            if (i >= g.d) break;
             float p[VEC];
-            in.products(j, tid, p);
+            in.products(i, p);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 const float t = p[e] * k;
-                if (tiny || fabsf(t - rintf(t)) > 0.5f - 0x1p-21f * fabsf(t)) todo |= 1u << (j * VEC + e);
+                if ((AL || i + e < g.d) && (tiny || fabsf(t - rintf(t)) > 0.5f - 0x1p-21f * fabsf(t))) todo |= 1u << (j * VEC + e);
             }
         }
     }
@@ -236,8 +229,8 @@ __device__ __noinline__ double q8_near(const Q8RowsArgs& g, const uint4* slot, i
     for (int round = 0; round < 2; ++round) {
         unsigned open = 0;
         for (unsigned left = todo; left; left &= left - 1) {
-            const int at = __ffs(left) - 1, j = at / VEC, e = at % VEC, i = in.index(j, tid) + e;
-            const double p = in.prod(j, tid, e);
+            const int at = __ffs(left) - 1, i = in.index(at / VEC, tid) + at % VEC;
+            const double p = in.prod(i);
             if (round == 0 && !exact) {
                 const float n = floorf(fabsf((float)p) * k);  // |t| lies within 2^-21 |t| of n + 1/2
                 const double diff = fabs(p) * 127.0 - ((double)n + 0.5) * (double)pmf;
@@ -260,13 +253,14 @@ __device__ __noinline__ double q8_near(const Q8RowsArgs& g, const uint4* slot, i
             if (nw > 1 && !(__uint_as_float(s_pm[t]) >= thr)) continue;
 #pragma unroll 1
             for (int j = 0; j < NV; ++j) {
-                if (in.index(j, 32 * t + lane) >= g.d) break;
+                const int i = in.index(j, 32 * t + lane);
+                if (i >= g.d) break;
                 float p[VEC];
-                in.products(j, 32 * t + lane, p);
+                in.products(i, p);
                 unsigned hit = 0;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) hit |= (fabsf(p[e]) >= thr ? 1u : 0u) << e;
-                for (; hit; hit &= hit - 1) dm = fmax(dm, fabs(in.prod(j, 32 * t + lane, __ffs(hit) - 1)));
+                for (int e = 0; e < VEC; ++e) hit |= ((AL || i + e < g.d) && fabsf(p[e]) >= thr ? 1u : 0u) << e;
+                for (; hit; hit &= hit - 1) dm = fmax(dm, fabs(in.prod(i + __ffs(hit) - 1)));
             }
         }
         dm = q8_warp_max(dm);
@@ -276,79 +270,145 @@ __device__ __noinline__ double q8_near(const Q8RowsArgs& g, const uint4* slot, i
 
 constexpr int kQ8RowSlots = 3;
 
-// NV pieces of VEC elements a thread: 16-byte vectors, or (VEC = 1) elements, for rows
-// that start at no vector boundary.  blockDim.x threads a row, and blockDim.y rows
-// a CTA when blockDim.x is one warp (no barrier then); CTAs walk the rows.
+// 16-byte blocks of shared memory for a row of one input (its last vector may reach into
+// one block more), and rows of inputs and outputs that a CTA's row needs.
+__host__ __device__ constexpr int q8_row_blocks(int nv, int threads) { return nv * threads + 1; }
+__host__ __device__ constexpr int q8_rows_kept(bool res, bool al) { return kQ8RowSlots * (res ? 2 : 1) + (al ? 0 : 1); }
+
+// NV vectors of 16 bytes a thread.  blockDim.x threads a row, and blockDim.y rows a CTA
+// when blockDim.x is one warp (no barrier then); CTAs walk the rows.
 //
-// Vectors come through shared memory by asynchronous copies, the next row's on the way
-// while this one is worked on (each thread copies what it reads itself, so no barrier
-// belongs to it).  The row's products stay in registers over the reduction, two
-// to an instruction throughout.  A row has one barrier; a warp can be one row ahead of
-// another, hence three slots and two sets of partials.  out_sum may be an input: with
-// VEC = 1 it is written last, when no warp reads the row from memory any more.
-template <int ESZ, int VEC, int NV, int MAXT, bool RES>
-__global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NV <= 2 || (VEC == 1 && NV <= 8) ? 4 : 3) : 1) sv_q8_rows(const __grid_constant__ Q8RowsArgs g)
+// Rows come through shared memory by asynchronous copies, the next row's on the way
+// while this one is worked on.  The row's products stay in registers over the
+// reduction, two to an instruction throughout.  A warp can be one row ahead of another,
+// hence three slots and two sets of partials.
+// AL: every row starts on a 16-byte boundary.  Each thread then copies what it reads
+// itself, and a row has one barrier.  Otherwise (d * ESZ not a multiple of 16) the
+// aligned blocks that hold the row are copied, a vector is read from the two it
+// lies in, and out_sum and out_normed are put together in shared memory to leave in
+// aligned blocks too (5000 x 4001 bf16 with a residual: 55 us, against 150 us element by
+// element).
+template <int ESZ, int NV, int MAXT, bool RES, bool AL>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NV <= 2 ? 4 : 3) : 1) sv_q8_rows(const __grid_constant__ Q8RowsArgs g)
 {
-    static_assert(VEC == 1 || VEC * ESZ == 16, "a piece is an element or a 16-byte vector");
-    constexpr int P = VEC > 1 ? VEC / 2 : 1;   // packed pairs of a vector
-    extern __shared__ __align__(16) unsigned char q8_rows_dyn[];  // VEC > 1: [slots][x, r][NV][threads] vectors
+    constexpr int VEC = 16 / ESZ, P = VEC / 2;  // packed pairs of a vector
+    constexpr int IN = RES ? 2 : 1;
+    extern __shared__ __align__(16) unsigned char q8_rows_dyn[];  // [slots][x, r][rows][blocks], then [rows][blocks] of output
     __shared__ float s_ss[2][32];
     __shared__ unsigned s_pm[2][32];
     __shared__ double s_sd[32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x, nw = nthr >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product may load its weights
-    constexpr int IN = RES ? 2 : 1;
-    const int all = nthr * blockDim.y;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x, nw = nthr >> 5;
     const int stride = gridDim.x * blockDim.y;
     const uint32_t one = ESZ == 2 ? 0x3f803f80u : 0x3f800000u;
-    uint4* const slots = reinterpret_cast<uint4*>(q8_rows_dyn) + threadIdx.y * nthr;
-    const int mine = cdiv_pos(g.d - tid * VEC, nthr * VEC);  // pieces of a row that this thread has (at most NV)
+    const int RB = q8_row_blocks(NV, nthr), in_step = blockDim.y * RB;  // blocks from an input to the next
+    uint4* const slots = reinterpret_cast<uint4*>(q8_rows_dyn) + threadIdx.y * RB;
+    uint4* const outs = slots + kQ8RowSlots * IN * in_step;
+    const int mine = cdiv_pos(g.d - tid * VEC, nthr * VEC);  // vectors of a row that this thread has (at most NV)
+    auto sync_row = [&] {
+        if (nw > 1) __syncthreads();
+        else __syncwarp();
+    };
 
-    // to slot `slot`, from byte `from` of the inputs (this thread's first element of a row)
-    auto copy = [&](size_t from, int slot) {
-        if (VEC == 1) return;
-        const uint32_t to = lr_smem(slots + slot * IN * NV * all + tid);
+    auto copy = [&](int row, int slot) {
+        const size_t at = (size_t)row * g.d * ESZ;
+        const unsigned sh = AL ? 0u : (unsigned)(at & 15u);
+        const uint32_t to = lr_smem(slots + slot * IN * in_step + tid);
+        const size_t from = at - sh + 16 * (size_t)tid;
         const char* x = static_cast<const char*>(g.x) + from;
         const char* r = RES ? static_cast<const char*>(g.r) + from : nullptr;
+        if (AL) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            if (j >= mine) break;
-            q8_cp16(to + 16 * j * all, x + 16 * (size_t)(j * nthr));
-            if (RES) q8_cp16(to + 16 * (NV + j) * all, r + 16 * (size_t)(j * nthr));
+            for (int j = 0; j < NV; ++j) {
+                if (j >= mine) break;
+                q8_cp16(to + 16 * j * nthr, x + 16 * (size_t)(j * nthr), 16);
+                if (RES) q8_cp16(to + 16 * (in_step + j * nthr), r + 16 * (size_t)(j * nthr), 16);
+            }
+        } else {
+            // the blocks that hold the row, none of them past the inputs' end
+            const int blocks = (int)((sh + (unsigned)g.d * ESZ + 15u) / 16u);
+            const size_t end = (size_t)g.M * g.d * ESZ;
+#pragma unroll
+            for (int j = 0; j <= NV; ++j) {
+                if (j * nthr + tid >= blocks) break;
+                const int bytes = (int)min((size_t)16, end - from - 16 * (size_t)(j * nthr));
+                q8_cp16(to + 16 * j * nthr, x + 16 * (size_t)(j * nthr), bytes);
+                if (RES) q8_cp16(to + 16 * (in_step + j * nthr), r + 16 * (size_t)(j * nthr), bytes);
+            }
+        }
+    };
+    // a row of output in index order, from shared memory to an unaligned row of global
+    auto flush = [&](void* to, size_t at) {
+        const unsigned sh = (unsigned)(at & 15u);
+        unsigned char* dst = static_cast<unsigned char*>(to) + (at - sh);
+        const int bytes = g.d * ESZ, blocks = (int)((sh + (unsigned)bytes + 15u) / 16u);
+        for (int b = tid; b < blocks; b += nthr) {
+            const int i = 16 * b - (int)sh;  // the row's byte that the block starts with
+            if (i >= 0 && i + 16 <= bytes) {
+                *reinterpret_cast<uint4*>(dst + 16 * (size_t)b) = sh ? shift16(outs[b - 1], outs[b], 16u - sh) : outs[b];
+            } else {
+                const unsigned char* src = reinterpret_cast<const unsigned char*>(outs);
+                for (int e = 0; e < 16; e += ESZ)
+                    if (i + e >= 0 && i + e < bytes) {
+                        if (ESZ == 2) *reinterpret_cast<unsigned short*>(dst + 16 * (size_t)b + e) = *reinterpret_cast<const unsigned short*>(src + i + e);
+                        else *reinterpret_cast<uint32_t*>(dst + 16 * (size_t)b + e) = *reinterpret_cast<const uint32_t*>(src + i + e);
+                    }
+            }
         }
     };
     // the weights, as packed as they came
-    uint4 wv[VEC > 1 ? NV : 1];
-    if (VEC > 1)
+    uint4 wv[NV];
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-            wv[j] = (g.w && j < mine) ? __ldg(reinterpret_cast<const uint4*>(g.w) + j * nthr + tid) : make_uint4(one, one, one, one);
+    for (int j = 0; j < NV; ++j) {
+        wv[j] = make_uint4(one, one, one, one);
+        const int i = (j * nthr + tid) * VEC;
+        if (!g.w || j >= mine) continue;
+        if (AL || i + VEC <= g.d) {
+            wv[j] = __ldg(reinterpret_cast<const uint4*>(g.w) + j * nthr + tid);
+        } else {
+            float w[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) w[e] = i + e < g.d ? q8_ld1<ESZ>(g.w, i + e) : 1.f;
+            wv[j] = q8_pack<ESZ>(w);
+        }
+    }
     int row = blockIdx.x * blockDim.y + threadIdx.y, slot = 0, set = 0;
-    size_t from = ((size_t)row * g.d + (size_t)tid * VEC) * ESZ;
-    const size_t from_step = (size_t)stride * g.d * ESZ;
-    if (row < g.M) copy(from, 0);
+    if (row < g.M) copy(row, 0);
     asm volatile("cp.async.commit_group;" ::: "memory");
-    for (; row < g.M; row += stride, from += from_step, slot = slot == kQ8RowSlots - 1 ? 0 : slot + 1, set ^= 1) {
+    for (; row < g.M; row += stride, slot = slot == kQ8RowSlots - 1 ? 0 : slot + 1, set ^= 1) {
         const size_t base = (size_t)row * g.d;
-        const Q8Row<ESZ, VEC, NV, RES> in64 = {g, slots + slot * IN * NV * all, all, row};  // elements in fp64
-        unsigned long long p2[VEC > 1 ? NV * P : 1];
-        float p1[VEC > 1 ? 1 : NV], s1[VEC > 1 ? 1 : NV];
+        const unsigned sh = AL ? 0u : (unsigned)(base * ESZ & 15u);
+        const uint4* in = slots + slot * IN * in_step;
+        const Q8Row<ESZ, RES, AL> in64 = {g, reinterpret_cast<const unsigned char*>(in) + sh, 16 * in_step};
+        if (row < g.M - stride) copy(row + stride, slot == kQ8RowSlots - 1 ? 0 : slot + 1);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        if (!AL) sync_row();  // the other threads' copies, and the last row's output has left
+        unsigned long long p2[NV * P];
         float tm = 0.f, ss;
-        if (VEC > 1) {
-            if (row < g.M - stride) copy(from + from_step, slot == kQ8RowSlots - 1 ? 0 : slot + 1);
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        {
             unsigned long long acc[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
             // (the weights stay packed from row to row: unpacked they take twice the registers)
 #pragma unroll
             for (int j = 0; j < NV; ++j) asm volatile("" : "+r"(wv[j].x), "+r"(wv[j].y), "+r"(wv[j].z), "+r"(wv[j].w));
+            auto get = [&](const uint4* at, int j) {
+                if (AL) return at[0];
+                uint4 v = shift16(at[0], at[1], sh);
+                const int n = (g.d - (j * nthr + tid) * VEC) * ESZ;  // bytes of the row from here on
+                if (n < 16) {
+                    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) w[q] = 4 * q >= n ? 0u : (ESZ == 2 && 4 * q + 2 >= n ? w[q] & 0xffffu : w[q]);
+                    v = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                return v;
+            };
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 uint4 x = make_uint4(0, 0, 0, 0), r = x;
                 if (j < mine) {
-                    const uint4* at = slots + (slot * IN * NV + j) * all + tid;
-                    x = *at;
-                    if (RES) r = at[NV * all];
+                    x = get(in + j * nthr + tid, j);
+                    if (RES) r = get(in + in_step + j * nthr + tid, j);
                 }
                 unsigned long long a[P], b[P], w[P];
                 q8_pairs<ESZ>(x, a);
@@ -369,26 +429,14 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NV <= 2 || (VEC == 1 && N
                 if (g.sum && j < mine) {  // (may be written over x or r: they are in shared memory)
                     float t[VEC];
 #pragma unroll
-                    for (int e = 0; e < P; ++e) unpack2(a[e], t[(2 * e) % VEC], t[(2 * e + 1) % VEC]);
-                    q8_st<ESZ, VEC>(g.sum, base + (size_t)(j * nthr + tid) * VEC, t);
+                    for (int e = 0; e < P; ++e) unpack2(a[e], t[2 * e], t[2 * e + 1]);
+                    if (AL) *reinterpret_cast<uint4*>(static_cast<char*>(g.sum) + (base + (size_t)(j * nthr + tid) * VEC) * ESZ) = q8_pack<ESZ>(t);
+                    else outs[j * nthr + tid] = q8_pack<ESZ>(t);
                 }
             }
             float u, v;
             unpack2(add2(acc[0], acc[1]), u, v);
             ss = u + v;
-        } else {
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int i = j * nthr + tid;
-                const bool in = i < g.d;
-                s1[j] = in ? q8_ld1<ESZ>(g.x, base + i) : 0.f;
-                if (in && RES) s1[j] += q8_ld1<ESZ>(g.r, base + i);
-                p1[j] = s1[j] * ((in && g.w) ? q8_ld1<ESZ>(g.w, i) : 1.f);
-                acc[j & 3] = fmaf(s1[j], s1[j], acc[j & 3]);
-                tm = q8_max3(tm, p1[j], 0.f);
-            }
-            ss = (acc[0] + acc[1]) + (acc[2] + acc[3]);
         }
         // sum s^2 and max |p| (as bits: NaN and inf order above every number)
         unsigned pm = __reduce_max_sync(0xffffffffu, __float_as_uint(tm));
@@ -408,6 +456,10 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NV <= 2 || (VEC == 1 && N
                 for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
             }
         }
+        if (!AL && g.sum) {
+            if (nw == 1) __syncwarp();
+            flush(g.sum, base * ESZ);
+        }
         const bool bad = pm >= 0x7f800000u;
         const float pmf = __uint_as_float(pm);
         const bool tiny = pmf < 0x1p-100f;  // 127 / pmf, or the products themselves, leave fp32: all in fp64
@@ -417,10 +469,10 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NV <= 2 || (VEC == 1 && N
         if (again) {
 #pragma unroll 1
             for (int j = 0; j < NV; ++j)
-                if ((j * nthr + tid) * VEC < g.d)
 #pragma unroll 1
-                    for (int e = 0; e < VEC; ++e) {
-                        const double s = in64.sum(j, tid, e);
+                for (int e = 0; e < VEC; ++e)
+                    if (in64.index(j, tid) + e < g.d) {
+                        const double s = in64.sum(in64.index(j, tid) + e);
                         sd += s * s;
                     }
             sd = q8_warp_sum(sd);
@@ -433,9 +485,9 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NV <= 2 || (VEC == 1 && N
         }
         // the integers
         const float k = 127.f * __frcp_rn(pmf);
-        uint32_t o[VEC > 1 ? NV * P / 2 : NV];
+        uint32_t o[NV * P / 2];
         float far = 0.f;  // the largest distance from an integer
-        if (VEC > 1) {
+        {
             const unsigned long long K2 = pack2(k, k), magic = pack2(0x1.8p23f, 0x1.8p23f);
 #pragma unroll
             for (int e = 0; e < NV * P; e += 2) {
@@ -450,14 +502,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NV <= 2 || (VEC == 1 && N
                     lo[h] = (uint32_t)m;
                     hi[h] = (uint32_t)(m >> 32);
                 }
-                o[e / 2] = __byte_perm(__byte_perm(lo[0], hi[0], 0x0040), __byte_perm(lo[1], hi[1], 0x0040), 0x5410);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const float t = p1[j] * k, n = rintf(t);
-                far = q8_max3(far, t - n, 0.f);
-                o[j] = (uint32_t)(int)n;
+                o[e / 2] = bad ? 0u : __byte_perm(__byte_perm(lo[0], hi[0], 0x0040), __byte_perm(lo[1], hi[1], 0x0040), 0x5410);
             }
         }
         int8_t* qrow = g.q + (size_t)row * g.ldq;
@@ -465,12 +510,13 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NV <= 2 || (VEC == 1 && N
         for (int j = 0; j < NV; ++j) {
             const int i = (j * nthr + tid) * VEC;
             if (j >= mine) break;
-            if (VEC == 1) {
-                qrow[i] = bad ? (int8_t)0 : (int8_t)o[j];
-            } else if (VEC > 4) {
-                *reinterpret_cast<uint2*>(qrow + i) = bad ? make_uint2(0, 0) : make_uint2(o[j * P / 2], o[j * P / 2 + (P > 2 ? 1 : 0)]);
+            if (AL || i + VEC <= g.d) {
+                if (VEC > 4) *reinterpret_cast<uint2*>(qrow + i) = make_uint2(o[j * P / 2], o[j * P / 2 + (P > 2 ? 1 : 0)]);
+                else *reinterpret_cast<uint32_t*>(qrow + i) = o[j * P / 2];
             } else {
-                *reinterpret_cast<uint32_t*>(qrow + i) = bad ? 0u : o[j * P / 2];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    if (i + e < g.d) qrow[i + e] = (int8_t)(o[j * P / 2 + e / 4] >> (8 * (e & 3)));
             }
         }
         double ms = 1.0;  // by all where g.normed, else by the first thread
@@ -478,40 +524,33 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NV <= 2 || (VEC == 1 && N
         if (g.normed) {
             const bool wide = !bad && (tiny || ms < 0x1p-200 || ms > 0x1p200);  // 1 / rms, or p, leaves fp32
             const float inv = bad ? NAN : (ms > 0.0 ? (float)(1.0 / sqrt(ms)) : 0.f);
+            if (!AL && g.sum) sync_row();  // the sums have left
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int i = (j * nthr + tid) * VEC;
                 if (j >= mine) break;
-                if (wide) {
-#pragma unroll 1
-                    for (int e = 0; e < VEC; ++e) q8_st1<ESZ>(g.normed, base + i + e, ms > 0.0 ? (float)(in64.prod(j, tid, e) / sqrt(ms)) : 0.f);
-                } else {
-                    float y[VEC];
-                    if (VEC > 1) {
+                float y[VEC];
 #pragma unroll
-                        for (int e = 0; e < P; ++e) unpack2(p2[j * P + e], y[(2 * e) % VEC], y[(2 * e + 1) % VEC]);
-                    } else {
-                        y[0] = p1[j];
-                    }
+                for (int e = 0; e < P; ++e) unpack2(p2[j * P + e], y[2 * e], y[2 * e + 1]);
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) y[e] *= inv;
-                    q8_st<ESZ, VEC>(g.normed, base + i, y);
-                }
+                for (int e = 0; e < VEC; ++e) y[e] *= inv;
+                if (wide)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) y[e] = ms > 0.0 && i + e < g.d ? (float)(in64.prod(i + e) / sqrt(ms)) : 0.f;
+                if (AL) *reinterpret_cast<uint4*>(static_cast<char*>(g.normed) + (base + i) * ESZ) = q8_pack<ESZ>(y);
+                else outs[j * nthr + tid] = q8_pack<ESZ>(y);
+            }
+            if (!AL) {
+                sync_row();
+                flush(g.normed, base * ESZ);
             }
         }
         // values whose rounding fp32 leaves open: seven roundings at most, so within
         // 8 * 2^-24 |t| of a half
         const bool near = !bad && (tiny || far > 0.5f - 0x1p-21f * tm * k);
         double dm = pmf;  // the maximum, as exactly as it is needed
-        if (__any_sync(0xffffffffu, near))
-            dm = q8_near<ESZ, VEC, NV, RES>(g, slots + slot * IN * NV * all, all, row, pmf, k, s_pm[set], near);
+        if (__any_sync(0xffffffffu, near)) dm = q8_near<ESZ, NV, RES, AL>(g, in64.x, in64.residual, row, pmf, k, s_pm[set], near);
         if (tid == 0) g.scale[row] = bad ? NAN : (dm > 0.0 ? (float)(dm / (127.0 * sqrt(ms))) : 0.f);
-        if (VEC == 1 && g.sum) {
-            if (nw > 1) __syncthreads();  // another warp may still read inputs of this one's from memory
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-                if (j < mine) q8_st1<ESZ>(g.sum, base + j * nthr + tid, s1[j]);
-        }
     }
 }
 
