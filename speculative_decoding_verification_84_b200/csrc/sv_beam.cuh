@@ -15,9 +15,9 @@
 //   sv_beam_pick   one CTA per row: the normaliser in fp64; the K best chunks, of
 //                  which it reads the logits again (K L vectors, from L2); the
 //                  logits at or above the K-th chunk's maximum (about K), ranked
-//                  by counting.  The CTA that finishes a sequence's last row finds
-//                  every candidate's place among the beams' sorted keys (fp64) by
-//                  binary search.  A programmatic dependent of sv_beam_rows.
+//                  by counting.  The CTA that finishes a sequence's last row places
+//                  the beams' candidates by their keys (fp64) the same way.  A
+//                  programmatic dependent of sv_beam_rows.
 // Selecting inside the pass (each CTA its segment's K best, with group maxima for
 // a threshold) cost more than the pass: 64 x 8 x 128256 bf16, K = 8, took 49 us in
 // that form against 27 us for the pass and 12 for the pick.
