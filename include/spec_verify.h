@@ -471,6 +471,8 @@ sv_status spec_verify_lowrank_head(const void* h, const void* w_down, const void
  * written.  K is at most SV_Q8_MAX_K, which keeps 128 * 128 * K below 2^31.
  */
 #define SV_Q8_MAX_K 131056
+/* Most rows of spec_verify_q8_quantize and spec_verify_q8_norm. */
+#define SV_Q8_MAX_M (1 << 30)
 
 /*
  * Rows to int8: out_scale[m] = max_k |x[m][k]| / 127 and out_q[m][k] =
@@ -510,6 +512,7 @@ sv_status spec_verify_q8_norm(const void* x, const void* residual, const void* w
  *   out [M][V] of dt (the logits spec_verify, spec_verify_tree and
  *   spec_verify_beam_select read), contiguous, 16-byte aligned
  *   out_error  optional, device int32: as for spec_verify_lowrank_up
+ * M and V such that ceil(M / 256) ceil(V / 128) <= 2^30, M at most SV_Q8_MAX_M.
  */
 sv_status spec_verify_q8_matmul(const int8_t* a, int lda, const float* a_scale, const int8_t* w, int ldw,
                                 const float* w_scale, int M, int K, int V, void* out, sv_dtype dt, int32_t* out_error,
@@ -548,9 +551,9 @@ size_t spec_verify_beam_workspace_size(int B, int W, int V, int K, sv_dtype dt);
  * in decreasing key, ties to the lower beam, then the lower token (inside a beam the
  * order is that of the logits).
  * T = 0: a beam's one candidate is its first argmax, with key score[b][w].
- * A frozen beam's one candidate is (pad_token, score[b][w]); its logits are not read.
- * A beam of score -inf, and a token of logit -inf, give no candidate (a first level:
- * score 0 for beam 0, -inf for the others).
+ * A frozen beam's one candidate is (pad_token, score[b][w]), whatever its logits.
+ * A beam of score -inf, whatever its logits, and a token of logit -inf give no candidate
+ * (a first level: score 0 for beam 0, -inf for the others).
  *   logits       [B][W][V] of dt, contiguous, 16-byte aligned
  *   score        [B][W] float;  temperature [B] float
  *   frozen       optional [B][W] int32, nonzero = frozen; pad_token in [0, V) then

@@ -110,7 +110,7 @@ sv_status q8_rows(const Q8RowsArgs& g, sv_dtype dt, cudaStream_t st)
 
 sv_status q8_rows_check(const void* x, sv_dtype dt, int M, int d, const void* q, int ldq, const void* scale)
 {
-    if (!x || !q || !scale || M < 1 || d < 1 || d > SV_Q8_MAX_K || ldq < d || ldq % 16) return SV_ERR_INVALID_ARG;
+    if (!x || !q || !scale || M < 1 || M > SV_Q8_MAX_M || d < 1 || d > SV_Q8_MAX_K || ldq < d || ldq % 16) return SV_ERR_INVALID_ARG;
     if (!dt_ok(dt)) return SV_ERR_UNSUPPORTED_DTYPE;
     if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4)) return SV_ERR_MISALIGNED;
     return SV_OK;
@@ -214,8 +214,6 @@ cudaError_t q8_gemm_launch(const void* a, long long lda, const void* w, long lon
     CUtensorMap tw, ta;
     if (!q8_map(&tw, w, g.V, g.K, ldw, kQ8BM) || !q8_map(&ta, a, g.M, g.K, lda, mine)) return cudaErrorInvalidValue;
     const long long tiles = (long long)g.m_tiles * g.v_tiles;
-    if (tiles + sms > 0x7fffffffLL || (long long)g.v_tiles * 2 * kQ8BM > 0x7fffffffLL || (long long)g.M + 1024 > 0x7fffffffLL)
-        return cudaErrorInvalidValue;
     const size_t smem = 1024 + (size_t)g.stages * g.sub * (kQ8WBytes + g.groups * mine * kQ8BK);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(pairs ? 2 * std::min<long long>(tiles, resident) : std::min<long long>(tiles, sms)));
@@ -263,7 +261,8 @@ sv_status q8_gemm_check(const void* a, int lda, const void* a_scale, const void*
                         int K, int V, const void* out, sv_dtype dt, const void* err)
 {
     if (!a || !a_scale || !w || !w_scale || !out || M < 1 || K < 1 || K > SV_Q8_MAX_K || V < 1 || V > SV_MAX_V ||
-        lda < K || lda % 16 || ldw < K || ldw % 16)
+        lda < K || lda % 16 || ldw < K || ldw % 16 || M > SV_Q8_MAX_M ||
+        cdiv(M, kQ8MaxNT) * cdiv(V, kQ8BM) > (1LL << 30))  // the tiles are counted in 32 bits
         return SV_ERR_INVALID_ARG;
     if (!dt_ok(dt)) return SV_ERR_UNSUPPORTED_DTYPE;
     if (!aligned(a, 16) || !aligned(w, 16) || !aligned(out, 16) || !aligned(a_scale, 4) || !aligned(w_scale, 4) ||
@@ -375,7 +374,7 @@ extern "C" sv_status spec_verify_q8_matmul(const int8_t* a, int lda, const float
 
 extern "C" size_t spec_verify_q8_head_workspace_size(int M, int d)
 {
-    if (M < 1 || d < 1 || d > SV_Q8_MAX_K) return 0;
+    if (M < 1 || M > SV_Q8_MAX_M || d < 1 || d > SV_Q8_MAX_K) return 0;
     return align256((size_t)M * (size_t)((d + 15) / 16 * 16)) + align256((size_t)M * sizeof(float));
 }
 

@@ -29,7 +29,7 @@ def _each(fn, good, cases):
 def test_quantize_refusals(lib):
     good = [GOOD, 1, 4, 40, GOOD, 48, GOOD, None]
     _each(lib.spec_verify_q8_quantize, good, [
-        (0, None, INVALID), (4, None, INVALID), (6, None, INVALID), (1, 2, DTYPE), (2, 0, INVALID), (2, -1, INVALID),
+        (0, None, INVALID), (4, None, INVALID), (6, None, INVALID), (1, 2, DTYPE), (2, 0, INVALID), (2, -1, INVALID), (2, (1 << 30) + 1, INVALID),
         (3, 0, INVALID), (3, binding.Q8_MAX_K + 1, INVALID), (5, 32, INVALID), (5, 47, INVALID), (5, 0, INVALID),
         (0, vp((1 << 20) + 8), MISALIGNED), (4, vp((1 << 20) + 8), MISALIGNED), (6, vp((1 << 20) + 2), MISALIGNED)])
 
@@ -47,8 +47,13 @@ def test_matmul_refusals(lib):
     _each(lib.spec_verify_q8_matmul, good, [
         *[(i, None, INVALID) for i in (0, 2, 3, 5, 9)], (1, 32, INVALID), (1, 47, INVALID), (4, 32, INVALID),
         (4, 56, INVALID), (6, 0, INVALID), (7, 0, INVALID), (7, binding.Q8_MAX_K + 1, INVALID), (8, 0, INVALID),
-        (10, 5, DTYPE), (0, vp(8), MISALIGNED), (3, vp(8), MISALIGNED), (9, vp(8), MISALIGNED), (2, vp(2), MISALIGNED),
+        (8, (1 << 30) + 1, INVALID), (6, (1 << 30) + 1, INVALID), (10, 5, DTYPE), (0, vp(8), MISALIGNED), (3, vp(8), MISALIGNED), (9, vp(8), MISALIGNED), (2, vp(2), MISALIGNED),
         (5, vp(2), MISALIGNED), (11, vp(2), MISALIGNED)])
+
+
+def test_matmul_refuses_more_tiles_than_it_counts(lib):
+    args = [GOOD, 48, GOOD, GOOD, 48, GOOD, 1 << 30, 40, 1 << 30, GOOD, 1, None, None]
+    assert lib.spec_verify_q8_matmul(*args) == INVALID
 
 
 def test_head_refusals(lib):

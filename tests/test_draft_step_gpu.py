@@ -89,6 +89,27 @@ def test_norm_shapes(M, d, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,d", [(2500, 4096), (2500, 1001), (12001, 72), (12001, 75), (900, 8200), (700, 16383)])
+def test_norm_many_rows(M, d, dtype):
+    """More rows than are worked on at once, out of place and in place."""
+    g = gen(M + d)
+    x, r = randn(g, M, d).to(dtype), (0.3 * randn(g, M, d)).to(dtype)
+    w = (1 + 0.1 * randn(g, d)).to(dtype)
+    q, scale, total, normed = _norm_case(x, r, w, 1e-6)
+    lib = binding.load_library()
+    for where in (0, 1):
+        xd, rd, wd = x.to(DEV), r.to(DEV), w.to(DEV)
+        q2 = torch.empty_strided(q.shape, q.stride(), dtype=q.dtype, device=DEV)
+        scale2 = torch.empty_like(scale)
+        to = (xd, rd)[where]
+        st = lib.spec_verify_q8_norm(xd.data_ptr(), rd.data_ptr(), wd.data_ptr(), 0 if dtype == torch.float32 else 1, 1e-6, M, d,
+                                     q2.data_ptr(), q2.stride(0), scale2.data_ptr(), to.data_ptr(), None,
+                                     torch.cuda.current_stream().cuda_stream)
+        assert st == 0
+        assert torch.equal(q2, q) and torch.equal(scale2, scale) and torch.equal(to, total)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("M,d", [(1, 1), (5, 96), (3, 1001), (2, 4096), (1, 131056)])
 def test_quantize_shapes(M, d, dtype):
     x = (randn(gen(d), M, d) * 0.02).to(dtype)
@@ -312,6 +333,36 @@ def test_select_ties(V, dtype):
     _check_select(z.to(dtype), torch.zeros(1, 1), torch.ones(1), 7, exact=True)
 
 
+@pytest.mark.parametrize("W,K", [(8, 32), (32, 32), (32, 5), (17, 31)])
+def test_select_ties_over_many_beams(W, K):
+    """More candidates than the last step ranks at once, all keys equal, or two values of
+    them, or none at all but a few."""
+    V = 300
+    flat = torch.zeros(3, W, V)
+    flat[1, :, ::2] = 1.0
+    flat[2] = float("-inf")
+    flat[2, :, 7] = 0.5
+    scores = torch.zeros(3, W)
+    scores[2, 1:] = float("-inf")
+    scores[2, W - 1] = 0.0
+    _check_select(flat, scores, torch.ones(3), K, exact=True)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [700, 40000, 128256])
+def test_select_sorted_logits(V, dtype):
+    """The best logits side by side at one end of the row, at the other, and in one place."""
+    up = torch.linspace(-8, 8, V)
+    bump = torch.full((V,), -5.0)
+    bump[V // 2 : V // 2 + 40] = torch.linspace(1, 5, 40)
+    rows = torch.stack([up, up.flip(0), bump]).to(dtype)
+    scores = torch.tensor([[0.0, -0.125, -0.25]])
+    for K in (1, 9, 32):
+        _check_select(rows[None], scores, torch.ones(1), K)
+    one = rows[:1].expand(1, 2, V).contiguous()
+    _check_select(one, torch.zeros(1, 2), torch.ones(1), 32, exact=True)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("V", [40, 3001, 33000])
 def test_select_masks(V, dtype):
@@ -335,7 +386,9 @@ def test_select_masks(V, dtype):
     np.testing.assert_array_equal(token.cpu().numpy(), wt)
     got = ref.f64(score)
     fin = wk > -1e38
-    assert (np.abs(got - wk)[fin] <= LSE + U * np.abs(wk[fin])).all()
+    with np.errstate(invalid="ignore"):
+        off = np.abs(got - wk)
+    assert (off[fin] <= LSE + U * np.abs(wk[fin])).all()
     assert (got[wk == -np.inf] == -np.inf).all() and (got[~fin] < -1e38).all()
 
 
