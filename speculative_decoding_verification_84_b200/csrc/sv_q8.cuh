@@ -876,40 +876,68 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         Q8Ring r, acc;
         int used = 0;  // accumulators so far, up to g.bufs
         bool ok = true;
+        // the products of stage place s, K blocks kb .., into accumulators h0 .. h1
+        uint32_t d[2];
+        auto products = [&](int s, int kb, int h0, int h1) {
+            uint64_t w = w0 + (uint64_t)((unsigned)(s * STAGE) >> 4);
+#pragma unroll
+            for (int u = 0; u < kQ8MaxSub; ++u, w += (unsigned)BLOCK >> 4) {
+                if (u >= SUB || kb + u >= kbs) break;
+#pragma unroll
+                for (int j = 0; j < kQ8BK / 32; ++j) {  // K = 32 per MMA: 32 bytes along the swizzled row
+                    const uint32_t on = (kb + u > 0 || j > 0) ? 1u : 0u;
+                    if (h0 == 0) q8_mma<PAIR>(d[0], w + 2 * j, w + a_off + 2 * j, idesc, on);
+                    if (h1 == 1) q8_mma<PAIR>(d[1], w + 2 * j, w + a_off + g_off + 2 * j, idesc, on);
+                }
+            }
+        };
         for (unsigned t = first; ok && t < tiles; t += step) {
-            uint32_t d[2];
             int buf[2];
-            for (int h = 0; h < G; ++h) {
+            unsigned parity[2];
+            bool taken[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (h >= G) break;
                 buf[h] = acc.s;
+                parity[h] = acc.phase ^ 1u;
+                taken[h] = used >= g.bufs;
                 d[h] = tmem + (uint32_t)(acc.s * g.buf_cols);
-                if (used >= g.bufs) ok = ok && q8_wait(&tempty[acc.s], acc.phase ^ 1u, abort, g.err);
-                else ++used;
+                used += taken[h] ? 0 : 1;
                 acc.next(g.bufs);
+            }
+            if (taken[0] && !q8_wait(&tempty[buf[0]], parity[0], abort, g.err)) { ok = false; break; }
+            lr_fence_after();
+            // while the second accumulator is still being stored, the first goes ahead through
+            // the stages of the ring
+            int ahead = 0;
+            if (G > 1 && taken[1] && !__all_sync(0xffffffffu, lr_try_wait(&tempty[buf[1]], parity[1]))) {
+                Q8Ring p = r;
+                for (int kb = 0; kb < kbs && ahead < S; kb += SUB, ++ahead) {
+                    ok = q8_wait(&full[p.s], p.phase, abort, g.err);
+                    if (!ok) break;
+                    lr_fence_after();
+                    if (q8_elect()) products(p.s, kb, 0, 0);
+                    __syncwarp();
+                    p.next(S);
+                }
+                ok = ok && q8_wait(&tempty[buf[1]], parity[1], abort, g.err);
             }
             if (!ok) break;
             lr_fence_after();
-            for (int kb = 0; kb < kbs; kb += SUB) {
-                if (!q8_wait(&full[r.s], r.phase, abort, g.err)) { ok = false; break; }
+            for (int kb = 0, n = 0; kb < kbs; kb += SUB, ++n) {
+                if (n >= ahead && !q8_wait(&full[r.s], r.phase, abort, g.err)) { ok = false; break; }
                 lr_fence_after();
                 if (q8_elect()) {
-                    uint64_t w = w0 + (uint64_t)((unsigned)(r.s * STAGE) >> 4);
-#pragma unroll
-                    for (int u = 0; u < kQ8MaxSub; ++u, w += (unsigned)BLOCK >> 4) {
-                        if (u >= SUB || kb + u >= kbs) break;
-#pragma unroll
-                        for (int j = 0; j < kQ8BK / 32; ++j) {  // K = 32 per MMA: 32 bytes along the swizzled row
-                            const uint32_t on = (kb + u > 0 || j > 0) ? 1u : 0u;
-                            q8_mma<PAIR>(d[0], w + 2 * j, w + a_off + 2 * j, idesc, on);
-                            if (G > 1) q8_mma<PAIR>(d[1], w + 2 * j, w + a_off + g_off + 2 * j, idesc, on);
-                        }
-                    }
+                    products(r.s, kb, n >= ahead ? 0 : 1, G - 1);
                     q8_commit<PAIR>(&empty[r.s]);
                 }
                 __syncwarp();
                 r.next(S);
             }
-            if (ok && q8_elect())
-                for (int h = 0; h < G; ++h) q8_commit<PAIR>(&tfull[buf[h]]);
+            if (ok && q8_elect()) {
+                q8_commit<PAIR>(&tfull[buf[0]]);
+                if (G > 1) q8_commit<PAIR>(&tfull[buf[1]]);
+            }
             __syncwarp();
         }
     } else if (warp >= 4) {
