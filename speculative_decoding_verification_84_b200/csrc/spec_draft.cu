@@ -317,12 +317,18 @@ cudaError_t beam_go(const BeamArgs& g, cudaStream_t st)
     cfg.gridDim = dim3((unsigned)(g.B * g.W));
     cfg.blockDim = dim3(kPickThreads);
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)g.W;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, sv_beam_pick<ESZ, AL>, g);
+    if (g.W == 1 || g.W > kPickCluster) return cudaLaunchKernelEx(&cfg, sv_beam_pick<ESZ, AL, false>, g);
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, sv_beam_pick<ESZ, AL, true>, g);
 }
 
 template <class VT>

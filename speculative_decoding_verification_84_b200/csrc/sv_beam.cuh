@@ -15,9 +15,9 @@
 //   sv_beam_pick   one CTA per row: the normaliser in fp64; the K best chunks, of
 //                  which it reads the logits again (K L vectors, from L2); the
 //                  logits at or above the K-th chunk's maximum (about K), ranked
-//                  by counting.  The CTA that finishes a sequence's last row places
-//                  the beams' candidates by their keys (fp64) the same way.  A
-//                  programmatic dependent of sv_beam_rows.
+//                  by counting.  The sequence's first CTA (or the last to finish)
+//                  places the beams' candidates by their keys (fp64) the same way.
+//                  A programmatic dependent of sv_beam_rows.
 // Selecting inside the pass (each CTA its segment's K best, with group maxima for
 // a threshold) cost more than the pass: 64 x 8 x 128256 bf16, K = 8, took 49 us in
 // that form against 27 us for the pass and 12 for the pick.
@@ -36,6 +36,7 @@ constexpr int kBeamThreads = 256;
 constexpr int kBeamNV = 8;          // vectors a lane and batch
 constexpr int kPickThreads = 128;
 constexpr int kPickWarps = kPickThreads / 32;
+constexpr int kPickCluster = 8;     // the most rows of a sequence that are one cluster
 constexpr int kBeamCap = 1024;      // candidates of a row, and a sequence's W K keys
 constexpr int kPickChunks = 64;     // chunks a row is looked for in without choosing among them
 
@@ -337,7 +338,23 @@ __device__ __forceinline__ int pick_rank(const unsigned long long* s_key, int n,
     return rank;
 }
 
-template <int ESZ, bool AL>
+// A value into the first CTA of the cluster's copy of a shared variable.
+__device__ __forceinline__ void pick_first(const void* p, double v)
+{
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\tst.shared::cluster.f64 [a], %1;\n\t}" ::"r"(beam_smem(p)), "d"(v)
+                 : "memory");
+}
+
+__device__ __forceinline__ void pick_first(const void* p, int v)
+{
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\tst.shared::cluster.u32 [a], %1;\n\t}" ::"r"(beam_smem(p)), "r"(v)
+                 : "memory");
+}
+
+// CL: the rows of a sequence are one cluster (W <= 8) and hand their candidates to its
+// first CTA's shared memory; otherwise through the workspace and a ticket (64 x 8 x 128256
+// bf16, K = 8: 39.3 us in all by ticket, 37.5 by cluster).
+template <int ESZ, bool AL, bool CL>
 __global__ void __launch_bounds__(kPickThreads) sv_beam_pick(BeamArgs g)
 {
     constexpr int VEC = 16 / ESZ, NU = 4, GROUPS = 64;
@@ -351,15 +368,29 @@ __global__ void __launch_bounds__(kPickThreads) sv_beam_pick(BeamArgs g)
     __shared__ int s_sel[kPickChunks];
     __shared__ float s_tau, s_low;
     __shared__ int s_n, s_m, s_last;
+    __shared__ double s_key[CL ? kPickCluster * SV_MAX_BEAMS : 1];  // CL, first CTA: [W][K]
+    __shared__ int s_tok[CL ? kPickCluster * SV_MAX_BEAMS : 1];
+    __shared__ int2 s_info[CL ? kPickCluster : 1];
+    if (CL) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // this CTA runs
     const int row = blockIdx.x, b = row / g.W, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int nch = g.nb * kBeamNV << (5 - g.Lsh), CH = VEC << g.Lsh, L = 1 << g.Lsh;
     const float T = __ldg(g.temperature + b), sc = __ldg(g.score + row);
     const bool frozen = g.frozen && __ldg(g.frozen + row), t_ok = beam_t_ok(T);
     float khi, klo;
     beam_k(t_ok ? T : 0.f, &khi, &klo);
-    double* key = g.key + (size_t)row * g.K;
-    int32_t* tok = g.tok + (size_t)row * g.K;
+    // candidate k of this row, and how many there are
+    auto keep = [&](int k, double key, int token) {
+        if (CL) {
+            const int c = (row - b * g.W) * g.K + k;
+            pick_first(&s_key[c], key);
+            pick_first(&s_tok[c], token);
+        } else {
+            g.key[(size_t)row * g.K + k] = key;
+            g.tok[(size_t)row * g.K + k] = token;
+        }
+    };
     if (tid == 0) { s_n = 0; s_m = 0; }
+    if (CL) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     int cnt = 0, bad = 0;
     if (!(sc < INFINITY)) {
@@ -367,7 +398,7 @@ __global__ void __launch_bounds__(kPickThreads) sv_beam_pick(BeamArgs g)
     } else if (sc == -INFINITY) {
     } else if (frozen) {
         cnt = 1;
-        if (tid == 0) { key[0] = (double)sc; tok[0] = g.pad_token; }
+        if (tid == 0) keep(0, (double)sc, g.pad_token);
     } else if (t_ok) {
         // ---- the chunks' maxima and the row's normaliser: batch sums against the largest
         // offset, in fp64
@@ -377,8 +408,12 @@ __global__ void __launch_bounds__(kPickThreads) sv_beam_pick(BeamArgs g)
 #pragma unroll 8
         for (int c = tid; c < nch; c += kPickThreads) best = fmaxf(best, cmax[c]);
         const float2 p0 = tid < g.nb ? part[tid] : make_float2(-INFINITY, 0.f);
+        const int want = T > 0.f ? g.K : 1;  // T = 0: all mass on the first argmax
+        // 64 groups of two threads, 32 of four where they bound the few wanted well enough
+        const int per = want <= 8 ? 4 : 2, groups = kPickThreads / per;
         m = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 1));
-        if ((lane & 1) == 0) s_group[tid >> 1] = m;
+        if (per == 4) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        if (tid % per == 0) s_group[tid / per] = m;
         m = beam_warp_max(m);
         if (lane == 0) s_top[warp] = m;
         __syncthreads();
@@ -386,15 +421,14 @@ __global__ void __launch_bounds__(kPickThreads) sv_beam_pick(BeamArgs g)
 #pragma unroll
         for (int i = 1; i < kPickWarps; ++i) top = fmaxf(top, s_top[i]);
         const float MK = beam_offset(top, khi);
-        const int want = T > 0.f ? g.K : 1;  // T = 0: all mass on the first argmax
         {
-            // the want-th largest of the 64 groups' maxima bounds the want-th chunk's from
-            // below; each warp places its own sixteen
-            const float x0 = s_group[lane], x1 = s_group[32 + lane];
-            const float mine = warp < 2 ? x0 : x1;
-            const int first = warp * (GROUPS / kPickWarps);
+            // the want-th largest of the groups' maxima bounds the want-th chunk's from
+            // below; each warp places its own quarter of them
+            const float x0 = s_group[lane], x1 = groups > 32 ? s_group[32 + lane] : -INFINITY;
+            const int first = warp * (groups / kPickWarps);
+            const float mine = first < 32 ? x0 : x1;
 #pragma unroll 4
-            for (int q = 0; q < GROUPS / kPickWarps; ++q) {
+            for (int q = 0; q < groups / kPickWarps; ++q) {
                 const int me = first + q;
                 const float y = __shfl_sync(0xffffffffu, mine, me & 31);
                 const unsigned b0 = __ballot_sync(0xffffffffu, x0 > y || (x0 == y && lane < me));
@@ -489,8 +523,7 @@ __global__ void __launch_bounds__(kPickThreads) sv_beam_pick(BeamArgs g)
             const double lse = s_lse;
             auto put = [&](int k, unsigned long long k1) {
                 const double l = (double)beam_unord((unsigned)(k1 >> 32));
-                key[k] = T > 0.f ? (double)sc + (l / (double)T - lse) : (double)sc;
-                tok[k] = (int)(0xffffffffu - (unsigned)k1);
+                keep(k, T > 0.f ? (double)sc + (l / (double)T - lse) : (double)sc, (int)(0xffffffffu - (unsigned)k1));
             };
             if (n <= kBeamCap) {
                 if (tid < 4) s_cand[n + tid] = 0ull;
@@ -515,9 +548,17 @@ __global__ void __launch_bounds__(kPickThreads) sv_beam_pick(BeamArgs g)
             }
         }
     }
-    if (tid == 0) g.row_info[row] = make_int2(cnt, bad);
-    // ---- the sequence's last row to finish joins them
-    if (g.W > 1) {
+    // ---- the sequence's first CTA, or the last one to finish, joins the rows
+    if (CL) {
+        if (tid == 0) {
+            pick_first(&s_info[row - b * g.W].x, cnt);
+            pick_first(&s_info[row - b * g.W].y, bad);
+        }
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        if (row != b * g.W) return;
+    } else if (g.W > 1) {
+        if (tid == 0) g.row_info[row] = make_int2(cnt, bad);
         __threadfence();
         __syncthreads();
         if (tid == 0) s_last = atomicAdd(g.ticket + b, 1u) == (unsigned)g.W - 1u;
@@ -525,6 +566,7 @@ __global__ void __launch_bounds__(kPickThreads) sv_beam_pick(BeamArgs g)
         if (!s_last) return;
         __threadfence();
     } else {
+        if (tid == 0) g.row_info[row] = make_int2(cnt, bad);
         __syncthreads();  // this row is the sequence
     }
     const size_t row0 = (size_t)b * g.W;
@@ -532,7 +574,7 @@ __global__ void __launch_bounds__(kPickThreads) sv_beam_pick(BeamArgs g)
     // longer needed; candidate c = w K + k, so ties go to the smaller c
     const int all = g.W * g.K;
     int* s_cnt = s_sel;
-    const int2 info = tid < g.W ? __ldcg(g.row_info + row0 + tid) : make_int2(0, 0);
+    const int2 info = tid < g.W ? (CL ? s_info[CL ? tid : 0] : __ldcg(g.row_info + row0 + tid)) : make_int2(0, 0);
     if (tid < g.W) s_cnt[tid] = info.x;
     if (warp == 0) {
         const unsigned st = __reduce_or_sync(0xffffffffu, (unsigned)info.y);
@@ -545,7 +587,7 @@ __global__ void __launch_bounds__(kPickThreads) sv_beam_pick(BeamArgs g)
         const int w = c / g.K;
         unsigned long long o = 0ull;
         if (c - w * g.K < s_cnt[w]) {
-            const unsigned long long u = (unsigned long long)__double_as_longlong(__ldcg(g.key + row0 * g.K + c) + 0.0);
+            const unsigned long long u = (unsigned long long)__double_as_longlong((CL ? s_key[CL ? c : 0] : __ldcg(g.key + row0 * g.K + c)) + 0.0);
             o = u ^ ((u >> 63) ? ~0ull : 0x8000000000000000ull);
         }
         s_cand[c] = o;
@@ -555,7 +597,7 @@ __global__ void __launch_bounds__(kPickThreads) sv_beam_pick(BeamArgs g)
         if (place >= g.K) return;
         const size_t at = (size_t)b * g.K + place;
         g.out_parent[at] = c / g.K;
-        g.out_token[at] = __ldcg(g.tok + row0 * g.K + c);
+        g.out_token[at] = CL ? s_tok[CL ? c : 0] : __ldcg(g.tok + row0 * g.K + c);
         g.out_score[at] = (float)__longlong_as_double((long long)(mine ^ ((mine >> 63) ? 0x8000000000000000ull : ~0ull)));
     };
     bool rank_all = all <= kPickThreads;
