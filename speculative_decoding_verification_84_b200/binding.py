@@ -7,7 +7,6 @@ tensors are not on a CUDA device, the call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import os
@@ -525,28 +524,31 @@ def _check_q8(t: torch.Tensor, name: str, rows: int, K: int, device) -> int:
     return ld
 
 
-@contextlib.contextmanager
-def _on_stream(device, stream):
-    with torch.cuda.device(device) if stream is None else torch.cuda.stream(stream):
-        yield torch.cuda.current_stream(device).cuda_stream
+def _here(device: torch.device, stream: torch.cuda.Stream | None):
+    """The current stream's handle; None where the tensors' device is not the current one
+    or the call names a stream, and has to be made inside ``_on``."""
+    if stream is None and torch.cuda.current_device() == device.index:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return None
 
 
 def _on(device: torch.device, stream: torch.cuda.Stream | None):
-    """A context with the tensors' device and the call's stream current (its value: the
-    stream's handle).  What is allocated inside belongs to that stream, so its memory is
-    not given away under a running kernel."""
-    if stream is None and torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext(torch._C._cuda_getCurrentRawStream(device.index))  # the common case, cheaply
-    if stream is not None and stream.device != device:
+    """A context with the tensors' device and the call's stream current.  What is allocated
+    inside belongs to that stream, so its memory is not given away under a running kernel."""
+    if stream is None:
+        return torch.cuda.device(device)
+    if stream.device != device:
         raise ValueError(f"the stream must be on {device}, got {stream.device}")
-    return _on_stream(device, stream)
+    return torch.cuda.stream(stream)
 
 
-def _q8_empty(like: torch.Tensor, rows: int, K: int):
-    """Int8 rows at a pitch that is a multiple of 16 bytes, and their scales."""
+def _q8_empty(x: torch.Tensor):
+    """Int8 rows of x's shape at a pitch that is a multiple of 16 bytes, and their scales."""
+    rows, K = x.shape
     ld = _q8_stride(K)
-    q = torch.empty_strided((rows, K), (ld, 1), dtype=torch.int8, device=like.device)
-    return q, like.new_empty((rows,), dtype=torch.float32), ld
+    q = torch.empty_like(x, dtype=torch.int8) if ld == K else \
+        torch.empty_strided((rows, K), (ld, 1), dtype=torch.int8, device=x.device)
+    return q, x.new_empty((rows,), dtype=torch.float32), ld
 
 
 def q8_quantize(x: torch.Tensor, *, stream: torch.cuda.Stream | None = None):
@@ -558,9 +560,12 @@ def q8_quantize(x: torch.Tensor, *, stream: torch.cuda.Stream | None = None):
     M, K = x.shape
     dt = _dt_code(x.dtype)
     _check(x, "x", None, (M, K), device)
-    with _on(device, stream) as s:
-        q, scale, ld = _q8_empty(x, M, K)
-        _raise_if(lib.spec_verify_q8_quantize(x.data_ptr(), dt, M, K, q.data_ptr(), ld, scale.data_ptr(), s))
+    s = _here(device, stream)
+    if s is None:
+        with _on(device, stream):
+            return q8_quantize(x)
+    q, scale, ld = _q8_empty(x)
+    _raise_if(lib.spec_verify_q8_quantize(x.data_ptr(), dt, M, K, q.data_ptr(), ld, scale.data_ptr(), s))
     return q, scale
 
 
@@ -579,15 +584,18 @@ def q8_norm(x: torch.Tensor, weight: torch.Tensor | None, eps: float, *, residua
         _check(weight, "weight", x.dtype, (d,), device)
     if residual is not None:
         _check(residual, "residual", x.dtype, (M, d), device)
-    with _on(device, stream) as s:
-        q, scale, ld = _q8_empty(x, M, d)
-        total = torch.empty_like(x) if residual is not None else None
-        normed = torch.empty_like(x) if with_normed else None
-        _raise_if(lib.spec_verify_q8_norm(x.data_ptr(), residual.data_ptr() if residual is not None else None,
-                                          weight.data_ptr() if weight is not None else None, dt, eps, M, d,
-                                          q.data_ptr(), ld, scale.data_ptr(),
-                                          total.data_ptr() if total is not None else None,
-                                          normed.data_ptr() if normed is not None else None, s))
+    s = _here(device, stream)
+    if s is None:
+        with _on(device, stream):
+            return q8_norm(x, weight, eps, residual=residual, with_normed=with_normed)
+    q, scale, ld = _q8_empty(x)
+    total = torch.empty_like(x) if residual is not None else None
+    normed = torch.empty_like(x) if with_normed else None
+    _raise_if(lib.spec_verify_q8_norm(x.data_ptr(), residual.data_ptr() if residual is not None else None,
+                                      weight.data_ptr() if weight is not None else None, dt, eps, M, d,
+                                      q.data_ptr(), ld, scale.data_ptr(),
+                                      total.data_ptr() if total is not None else None,
+                                      normed.data_ptr() if normed is not None else None, s))
     out = (q, scale)
     if total is not None:
         out += (total,)
@@ -613,10 +621,13 @@ def q8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: 
     if error is not None:
         _check(error, "error", torch.int32, (1,), device)
     dt = _dt_code(dtype)
-    with _on(device, stream) as s:
-        z = a.new_empty((M, V), dtype=dtype)
-        _raise_if(lib.spec_verify_q8_matmul(a.data_ptr(), lda, a_scale.data_ptr(), w.data_ptr(), ldw, w_scale.data_ptr(),
-                                            M, K, V, z.data_ptr(), dt, error.data_ptr() if error is not None else None, s))
+    s = _here(device, stream)
+    if s is None:
+        with _on(device, stream):
+            return q8_matmul(a, a_scale, w, w_scale, dtype, error=error)
+    z = a.new_empty((M, V), dtype=dtype)
+    _raise_if(lib.spec_verify_q8_matmul(a.data_ptr(), lda, a_scale.data_ptr(), w.data_ptr(), ldw, w_scale.data_ptr(),
+                                        M, K, V, z.data_ptr(), dt, error.data_ptr() if error is not None else None, s))
     return z
 
 
@@ -642,16 +653,19 @@ def q8_head(x: torch.Tensor, weight: torch.Tensor | None, eps: float, w: torch.T
         _check(error, "error", torch.int32, (1,), device)
     if workspace is not None:
         _check(workspace, "workspace", torch.uint8, (workspace.numel(),), device)
-    with _on(device, stream) as s:
-        if workspace is None:
-            workspace = torch.empty(lib.spec_verify_q8_head_workspace_size(M, d), dtype=torch.uint8, device=device)
-        z = torch.empty((M, V), dtype=dtype, device=device)
-        total = torch.empty_like(x) if residual is not None else None
-        _raise_if(lib.spec_verify_q8_head(x.data_ptr(), residual.data_ptr() if residual is not None else None,
-                                          weight.data_ptr() if weight is not None else None, xdt, eps, w.data_ptr(), ldw,
-                                          w_scale.data_ptr(), M, d, V, total.data_ptr() if total is not None else None,
-                                          z.data_ptr(), dt, workspace.data_ptr(), workspace.numel(),
-                                          error.data_ptr() if error is not None else None, s))
+    s = _here(device, stream)
+    if s is None:
+        with _on(device, stream):
+            return q8_head(x, weight, eps, w, w_scale, dtype, residual=residual, workspace=workspace, error=error)
+    if workspace is None:
+        workspace = torch.empty(lib.spec_verify_q8_head_workspace_size(M, d), dtype=torch.uint8, device=device)
+    z = torch.empty((M, V), dtype=dtype, device=device)
+    total = torch.empty_like(x) if residual is not None else None
+    _raise_if(lib.spec_verify_q8_head(x.data_ptr(), residual.data_ptr() if residual is not None else None,
+                                      weight.data_ptr() if weight is not None else None, xdt, eps, w.data_ptr(), ldw,
+                                      w_scale.data_ptr(), M, d, V, total.data_ptr() if total is not None else None,
+                                      z.data_ptr(), dt, workspace.data_ptr(), workspace.numel(),
+                                      error.data_ptr() if error is not None else None, s))
     return z if total is None else (z, total)
 
 
@@ -684,18 +698,22 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, temperature: torch.T
     if need == 0:
         raise SpecVerifyError(1, f"beam_select takes W and K in [1, {MAX_BEAMS}], V in [1, {1 << 20}] and B >= 1; got "
                                  f"B={B}, W={W}, V={V}, K={K}")
-    with _on(device, stream) as s:
-        if workspace is None:
-            workspace = logits.new_empty((need,), dtype=torch.uint8)
-        parent = scores.new_empty((B, K), dtype=torch.int32)
-        token = scores.new_empty((B, K), dtype=torch.int32)
-        score = scores.new_empty((B, K))
-        status = scores.new_empty((B,), dtype=torch.int32) if return_row_status else None
-        _raise_if(lib.spec_verify_beam_select(logits.data_ptr(), dt, scores.data_ptr(), temperature.data_ptr(),
-                                              frozen.data_ptr() if frozen is not None else None, int(pad_token), B, W, V,
-                                              K, parent.data_ptr(), token.data_ptr(), score.data_ptr(),
-                                              status.data_ptr() if status is not None else None, workspace.data_ptr(),
-                                              workspace.numel(), s))
+    s = _here(device, stream)
+    if s is None:
+        with _on(device, stream):
+            return beam_select(logits, scores, temperature, K, frozen=frozen, pad_token=pad_token,
+                               return_row_status=return_row_status, workspace=workspace)
+    if workspace is None:
+        workspace = logits.new_empty((need,), dtype=torch.uint8)
+    parent = scores.new_empty((B, K), dtype=torch.int32)
+    token = torch.empty_like(parent)
+    score = scores.new_empty((B, K))
+    status = scores.new_empty((B,), dtype=torch.int32) if return_row_status else None
+    _raise_if(lib.spec_verify_beam_select(logits.data_ptr(), dt, scores.data_ptr(), temperature.data_ptr(),
+                                          frozen.data_ptr() if frozen is not None else None, int(pad_token), B, W, V,
+                                          K, parent.data_ptr(), token.data_ptr(), score.data_ptr(),
+                                          status.data_ptr() if status is not None else None, workspace.data_ptr(),
+                                          workspace.numel(), s))
     out = (parent, token, score)
     return out + (status,) if return_row_status else out
 
@@ -719,12 +737,15 @@ def beam_reorder(src: torch.Tensor, parent: torch.Tensor, *, out: torch.Tensor |
         _check(lengths, "lengths", torch.int32, (B,), device)
     if out is not None:
         _check(out, "out", src.dtype, (L, B, K, H, S, D), device)
-    with _on(device, stream) as s:
-        if out is None:
-            out = torch.zeros((L, B, K, H, S, D), dtype=src.dtype, device=device)
-        _raise_if(lib.spec_verify_beam_reorder(src.data_ptr(), out.data_ptr(), parent.data_ptr(),
-                                               lengths.data_ptr() if lengths is not None else None, L, B, W, K, H, S,
-                                               D * src.element_size(), s))
+    s = _here(device, stream)
+    if s is None:
+        with _on(device, stream):
+            return beam_reorder(src, parent, out=out, lengths=lengths)
+    if out is None:
+        out = torch.zeros((L, B, K, H, S, D), dtype=src.dtype, device=device)
+    _raise_if(lib.spec_verify_beam_reorder(src.data_ptr(), out.data_ptr(), parent.data_ptr(),
+                                           lengths.data_ptr() if lengths is not None else None, L, B, W, K, H, S,
+                                           D * src.element_size(), s))
     return out
 
 

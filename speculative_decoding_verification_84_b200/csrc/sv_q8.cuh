@@ -68,12 +68,11 @@ __device__ __forceinline__ void q8_st1(void* p, size_t i, float v)
 template <int ESZ>
 __device__ __forceinline__ uint4 q8_pack(const float* v)
 {
-    if (ESZ == 4) return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
     uint32_t o[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const __nv_bfloat162 h = __floats2bfloat162_rn(v[(2 * e) % (16 / ESZ)], v[(2 * e + 1) % (16 / ESZ)]);
-        o[e] = *reinterpret_cast<const uint32_t*>(&h);
+        o[e] = ESZ == 4 ? __float_as_uint(v[e]) : *reinterpret_cast<const uint32_t*>(&h);
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
