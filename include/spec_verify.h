@@ -563,7 +563,8 @@ size_t spec_verify_beam_workspace_size(int B, int W, int V, int K, sv_dtype dt);
  *   out_row_status  optional [B] int32: SV_ROW_BAD_TEMPERATURE (nothing but frozen
  *                beams is considered), SV_ROW_BAD_LOGITS (a row that is read holds NaN
  *                or +inf, is all -inf, or its logits / T leave fp32's range from
- *                above, or all of them from below), SV_ROW_BAD_SCORE (NaN or +inf); a
+ *                above, or all of them from below; finite ones inside it are taken
+ *                whatever their size, mask values like -1e30 among them), SV_ROW_BAD_SCORE (NaN or +inf); a
  *                beam at fault gives no candidate.
  * Limits: W and K in [1, SV_MAX_BEAMS], V in [1, SV_BEAM_MAX_V].  Two launches.
  * spec_verify_tree's output law is the target's for children drawn independently

@@ -65,6 +65,12 @@ __device__ __forceinline__ bool beam_t_ok(float T) { return T == 0.f || (T >= SV
 
 // Integer offset of a batch's sum: of its maximum, kept finite where a batch holds only
 // the type's lowest values (its sum is then 0).  T = 0 (khi = 1) needs the NaN test only.
+// Up to kBeamOffset the offset is within 32 of the maximum's exponent (fp32 steps by 16 or
+// 32 there, and klo adds up to 16), so a batch's sum lies in fp32's range and keeps terms
+// down to 2^-94 of the largest.  Beyond it the sum may be anything, 0 or infinite
+// included: such a batch counts for nothing beside a maximum within the bound, and
+// where the row's own maximum is beyond it the normaliser is taken again in fp64.
+constexpr float kBeamOffset = 0x1p28f;
 __device__ __forceinline__ float beam_offset(float m, float khi)
 {
     return m == -INFINITY ? 0.f : fmaxf(ceilf(__fmul_rn(m, khi)), -3e38f);
@@ -338,6 +344,38 @@ __device__ __forceinline__ int pick_rank(const unsigned long long* s_key, int n,
     return rank;
 }
 
+// log(sum exp((l - top) / T)) of a row by the whole CTA, in fp64 and in a fixed order: for
+// rows whose logits / T are beyond what the pass's offsets hold.  NaN where the row has
+// one, or top / T leaves fp32's range.  64 x 8 x 128256 bf16 with every row such a one: 133
+// us a selection, against 39 with none.
+template <int ESZ, bool AL>
+__device__ __noinline__ double pick_lse_wide(const BeamArgs& g, int row, float top, float T, double* s_sum)
+{
+    constexpr int VEC = 16 / ESZ;
+    const unsigned char* base = static_cast<const unsigned char*>(g.logits);
+    const unsigned char* end = base + (size_t)g.B * g.W * g.V * ESZ;
+    const double inv = 1.0 / (double)T;
+    double S = fabs((double)top / (double)T) <= FLT_MAX ? 0.0 : NAN;
+#pragma unroll 1
+    for (int i = threadIdx.x * VEC; i < g.V; i += kPickThreads * VEC) {
+        float x[VEC];
+        unpack<ESZ>(beam_ld<ESZ, AL>(base + (size_t)row * g.V * ESZ, i, g.V, end), x);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const double y = ((double)x[e] - (double)top) * inv;
+            if (!(y < -746.0)) S += exp(y);  // below that exp is 0; NaN is taken
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
+    __syncthreads();  // s_sum's earlier values have been read
+    if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = S;
+    __syncthreads();
+    S = s_sum[0];
+    for (int i = 1; i < kPickWarps; ++i) S += s_sum[i];
+    return log(S);
+}
+
 // A value into the first CTA of the cluster's copy of a shared variable.
 __device__ __forceinline__ void pick_first(const void* p, double v)
 {
@@ -355,7 +393,7 @@ __device__ __forceinline__ void pick_first(const void* p, int v)
 // first CTA's shared memory; otherwise through the workspace and a ticket (64 x 8 x 128256
 // bf16, K = 8: 39.3 us in all by ticket, 37.5 by cluster).
 template <int ESZ, bool AL, bool CL>
-__global__ void __launch_bounds__(kPickThreads) sv_beam_pick(BeamArgs g)
+__global__ void __launch_bounds__(kPickThreads) sv_beam_pick(const __grid_constant__ BeamArgs g)
 {
     constexpr int VEC = 16 / ESZ, NU = 4, GROUPS = 64;
     __shared__ float s_group[GROUPS];
@@ -438,8 +476,10 @@ __global__ void __launch_bounds__(kPickThreads) sv_beam_pick(BeamArgs g)
         }
         double S = 0.0;
         {
+            // (a batch without weight may hold an infinite sum; NaN stays)
             auto add = [&](const float2& p) {
-                S += (double)p.y * (p.x == -INFINITY ? 1.0 : pow2d(beam_offset(p.x, khi) - MK));
+                const double weight = p.x == -INFINITY ? 1.0 : pow2d(beam_offset(p.x, khi) - MK);
+                if (weight > 0.0 || p.y != p.y) S += (double)p.y * weight;
             };
             add(p0);
             for (int t = tid + kPickThreads; t < g.nb; t += kPickThreads) add(part[t]);
@@ -451,15 +491,19 @@ __global__ void __launch_bounds__(kPickThreads) sv_beam_pick(BeamArgs g)
         S = s_sum[0];
 #pragma unroll
         for (int i = 1; i < kPickWarps; ++i) S += s_sum[i];
-        // (a NaN or +inf makes S NaN; an all -inf batch has sum 0)
-        if (!(top > -INFINITY && top < INFINITY) || S != S || (T > 0.f && !(S > 0.0 && S <= DBL_MAX && MK <= FLT_MAX))) {
+        // (a NaN makes S NaN; an all -inf batch has sum 0)
+        const bool finite = top > -INFINITY && top < INFINITY;
+        const bool wide = T > 0.f && finite && !(fabsf(MK) <= kBeamOffset);
+        if (wide) S = pick_lse_wide<ESZ, AL>(g, row, top, T, s_sum);
+        if (!finite || S != S) {
             bad = SV_ROW_BAD_LOGITS;
         } else {
             // ---- the chunks that hold the `want` best logits: those at or above the bound, a
             // few more than `want`; where ties make them many, exactly the `want` best
-            // (and, meanwhile, the normaliser's logarithm)
+            // (and, meanwhile, the normaliser's logarithm, of logits taken from `ref`)
             const float tau = s_tau;
-            if (tid == kPickThreads - 1) s_lse = ((double)MK + log2(S)) * kLn2;
+            const double ref = wide ? (double)top : 0.0;
+            if (tid == kPickThreads - 1) s_lse = wide ? S : ((double)MK + log2(S)) * kLn2;
             if (best >= tau) {
                 for (int c = tid; c < nch; c += kPickThreads) {
                     const float x = cmax[c];
@@ -523,7 +567,7 @@ __global__ void __launch_bounds__(kPickThreads) sv_beam_pick(BeamArgs g)
             const double lse = s_lse;
             auto put = [&](int k, unsigned long long k1) {
                 const double l = (double)beam_unord((unsigned)(k1 >> 32));
-                keep(k, T > 0.f ? (double)sc + (l / (double)T - lse) : (double)sc, (int)(0xffffffffu - (unsigned)k1));
+                keep(k, T > 0.f ? (double)sc + ((l - ref) / (double)T - lse) : (double)sc, (int)(0xffffffffu - (unsigned)k1));
             };
             if (n <= kBeamCap) {
                 if (tid < 4) s_cand[n + tid] = 0ull;
