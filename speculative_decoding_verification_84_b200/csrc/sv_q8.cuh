@@ -703,6 +703,8 @@ struct Q8Ring {
 // The logits of channel v (one a lane) and the accumulator's tokens m0 .., from TMEM at
 // acc: 16-column chunks grp, grp + 4, ...  A bf16 row of even length goes out in words:
 // two lanes trade a value, so each stores a channel pair of one of two tokens.
+// The tokens' scales may have been written while this kernel was already running (it can
+// be a programmatic dependent of the norm), so they are not read as constant memory.
 template <int ESZ>
 __device__ __forceinline__ void q8_epilogue(const Q8GemmArgs& g, uint32_t acc, int grp, int m0, int v)
 {
@@ -717,10 +719,10 @@ __device__ __forceinline__ void q8_epilogue(const Q8GemmArgs& g, uint32_t acc, i
         if (wide && left >= 16) {
 #pragma unroll
             for (int j = 0; j < 16; j += 4)
-                *reinterpret_cast<float4*>(sa + j) = __ldg(reinterpret_cast<const float4*>(g.a_scale + m0 + c + j));
+                *reinterpret_cast<float4*>(sa + j) = *reinterpret_cast<const float4*>(g.a_scale + m0 + c + j);
         } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) sa[j] = j < left ? __ldg(g.a_scale + m0 + c + j) : 0.f;
+            for (int j = 0; j < 16; ++j) sa[j] = j < left ? g.a_scale[m0 + c + j] : 0.f;
         }
         uint32_t r[16];
         q8_tmem_ld16(acc + (uint32_t)c, r);

@@ -112,3 +112,24 @@ def test_head_forms(M, d, V, xdt, dtype):
         assert torch.equal(total, total2)
         assert torch.equal(z, binding.q8_matmul(q, scale, w, ws, dtype))
     _check(z, q, scale, w, ws)
+
+
+@pytest.mark.parametrize("xdt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,d,V", [(1, 512, 1000), (64, 1024, 2001)])
+def test_heads_in_a_row_share_a_workspace(M, d, V, xdt):
+    """Calls one after the other, each with other hidden states, in one workspace: the
+    product of each reads the integers and scales that its own norm left there."""
+    g = _gen(M, d, V)
+    wq, ws = binding.q8_quantize((torch.randn((V, d), generator=g) / 16).to(DEV))
+    lib = binding.load_library()
+    work = torch.empty(lib.spec_verify_q8_head_workspace_size(M, d), dtype=torch.uint8, device=DEV)
+    xs = [(torch.randn((M, d), generator=g) * 4.0 ** (i % 5 - 2)).to(xdt).to(DEV) for i in range(16)]
+    want = []
+    for x in xs:
+        q, scale = binding.q8_norm(x, None, 1e-6)
+        want.append(binding.q8_matmul(q, scale, wq, ws))
+    torch.cuda.synchronize()
+    for _ in range(4):
+        got = [binding.q8_head(x, None, 1e-6, wq, ws, workspace=work) for x in xs]
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
