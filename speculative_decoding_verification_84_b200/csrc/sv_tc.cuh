@@ -40,6 +40,20 @@ __device__ __forceinline__ bool lr_try_wait(uint64_t* bar, unsigned parity)
     return ok != 0;
 }
 
+// Whether the phase with this parity has completed, without suspending.
+__device__ __forceinline__ bool lr_test(uint64_t* bar, unsigned parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(lr_smem(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Wait for the phase with this parity; false (after raising the flags) if it did
 // not complete within kLrPolls polls, or another role of the CTA already gave up.
 __device__ __forceinline__ bool lr_wait(uint64_t* bar, unsigned parity, volatile int* abort, int* err)
