@@ -462,8 +462,8 @@ sv_status spec_verify_lowrank_head(const void* h, const void* w_down, const void
  * The draft's full-rank head in 8-bit integers, in place of the low-rank one: the
  * last hidden states are normed and quantised, a scale for each token, and
  * multiplied with weights quantised once, a scale for each channel.  Products and
- * sums are exact (int32), so the rounding of a logit comes from its two scales and
- * its output type alone.  Infrastructure around [SlimSpec, Metodologia,
+ * sums are exact (int32); a logit's roundings are those of the sum to fp32, of the two
+ * multiplications by its scales, and of its output type.  Infrastructure around [SlimSpec, Metodologia,
  * "Arquitetura": the draft's LM head W_full h]; the pages give no 8-bit form.
  *
  * An int8 matrix [rows][K] has a row pitch ld (bytes): a multiple of 16, at least K
@@ -506,8 +506,9 @@ sv_status spec_verify_q8_norm(const void* x, const void* residual, const void* w
                               struct CUstream_st* stream);
 
 /*
- * out[m][v] = a_scale[m] * w_scale[v] * sum_k a[m][k] * w[v][k], rounded once to dt,
- * on the tensor cores.
+ * out[m][v] = a_scale[m] * w_scale[v] * sum_k a[m][k] * w[v][k] on the tensor cores: within
+ * 3 * 2^-24 of it, relative (or 2^-149, below fp32's normal range), then rounded to dt.
+ * Scales may lie anywhere in fp32's range.
  *   a [M][lda], w [V][ldw] int8;  a_scale [M], w_scale [V] float
  *   out [M][V] of dt (the logits spec_verify, spec_verify_tree and
  *   spec_verify_beam_select read), contiguous, 16-byte aligned

@@ -705,6 +705,11 @@ struct Q8Ring {
 // two lanes trade a value, so each stores a channel pair of one of two tokens.
 // The tokens' scales may have been written while this kernel was already running (it can
 // be a programmatic dependent of the norm), so they are not read as constant memory.
+// Three fp32 roundings: the sum, the sum times one scale, that times the other.  A channel's
+// scale of at most 1 goes first: the sum times it cannot overflow, and is within a
+// rounding of exact down to the least subnormal (an integer times one).  A larger one goes
+// last: what overflows before it is beyond fp32's range after it as well.  (The two scales'
+// own product may leave the range where the logit does not.)
 template <int ESZ>
 __device__ __forceinline__ void q8_epilogue(const Q8GemmArgs& g, uint32_t acc, int grp, int m0, int v)
 {
@@ -713,6 +718,7 @@ __device__ __forceinline__ void q8_epilogue(const Q8GemmArgs& g, uint32_t acc, i
     const bool words = ESZ == 2 && (g.V & 1) == 0;
     const bool wide = (reinterpret_cast<uintptr_t>(g.a_scale) & 15u) == 0;
     const int odd = v & 1;
+    const bool sw_first = fabsf(sw) <= 1.f;
     for (int c = grp * 16; c < g.nt && m0 + c < g.M; c += 4 * kQ8EpiWarps) {
         const int left = g.M - (m0 + c);  // tokens from here on
         float sa[16];
@@ -727,10 +733,15 @@ __device__ __forceinline__ void q8_epilogue(const Q8GemmArgs& g, uint32_t acc, i
         uint32_t r[16];
         q8_tmem_ld16(acc + (uint32_t)c, r);
         float z[16];
+        if (__all_sync(0xffffffffu, sw_first)) {
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-            const unsigned long long p = pack2((float)(int)r[j], (float)(int)r[j + 1]);
-            unpack2(mul2(p, mul2(pack2(sa[j], sa[j + 1]), sw2)), z[j], z[j + 1]);
+            for (int j = 0; j < 16; j += 2) {
+                const unsigned long long p = pack2((float)(int)r[j], (float)(int)r[j + 1]);
+                unpack2(mul2(mul2(p, sw2), pack2(sa[j], sa[j + 1])), z[j], z[j + 1]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) z[j] = (float)(int)r[j] * (sw_first ? sw : sa[j]) * (sw_first ? sa[j] : sw);
         }
         const bool in = v < g.V;  // (the others still take part in the loads and the trade)
         if (words) {
