@@ -198,6 +198,57 @@ struct Q8Row {
     }
 };
 
+// Whether a product of the row's part of thread t is not zero, although fp32 may have made
+// it so.  The vectors of a padding row are told by their bits.
+template <int ESZ, int NV, bool RES, bool AL>
+__device__ __forceinline__ bool q8_some_product(const Q8Row<ESZ, RES, AL>& in, int t)
+{
+    constexpr int VEC = 16 / ESZ;
+    constexpr uint32_t digits = ESZ == 2 ? 0x7fff7fffu : 0x7fffffffu;
+    bool some = false;
+#pragma unroll 1
+    for (int j = 0; j < NV; ++j) {
+        const int i = in.index(j, t);
+        if (i >= in.g.d) break;
+        if (AL) {
+            const uint4 a = *reinterpret_cast<const uint4*>(in.x + i * ESZ);
+            const uint4 b = RES ? *reinterpret_cast<const uint4*>(in.x + in.residual + i * ESZ) : make_uint4(0, 0, 0, 0);
+            if (((a.x | a.y | a.z | a.w | b.x | b.y | b.z | b.w) & digits) == 0u) continue;
+        }
+#pragma unroll 1
+        for (int e = 0; e < VEC && i + e < in.g.d; ++e) some |= in.prod(i + e) != 0.0;
+    }
+    return some;
+}
+
+// Whether a row whose products are all zero in fp32 is one of zeros (padding, as a rule): its
+// integers are then written.  Each warp answers for its part, the first, whose thread has
+// use for the maximum, for the whole row.  16384 x 4096 bf16 of zeros with a residual: 143 us;
+// 1360 by q8_near, which takes every element of a row of tiny values in fp64.
+template <int ESZ, int NV, bool RES, bool AL>
+__device__ __noinline__ bool q8_zero_row(const Q8RowsArgs& g, const unsigned char* x, int residual, int row)
+{
+    constexpr int VEC = 16 / ESZ;
+    const Q8Row<ESZ, RES, AL> in = {g, x, residual};
+    const int tid = threadIdx.x, lane = tid & 31;
+    int8_t* qrow = g.q + (size_t)row * g.ldq;
+    __syncwarp();  // one warp a row: the other lanes' copies
+    int t = tid & ~31;
+    const int last = tid < 32 ? (int)blockDim.x - 32 : t;
+    for (; t <= last; t += 32)
+        if (__any_sync(0xffffffffu, q8_some_product<ESZ, NV, RES, AL>(in, t + lane))) return false;
+    for (int j = 0; j < NV; ++j) {
+        const int i = in.index(j, tid);
+        if (i + VEC <= g.d) {
+            if (VEC > 4) *reinterpret_cast<uint2*>(qrow + i) = make_uint2(0u, 0u);
+            else *reinterpret_cast<uint32_t*>(qrow + i) = 0u;
+        } else {
+            for (int e = 0; i + e < g.d; ++e) qrow[i + e] = 0;
+        }
+    }
+    return true;
+}
+
 // The values of a warp's part of a row whose rounding fp32 leaves open, decided exactly
 // and written again: first 127 |p| against (n + 1/2) max with the fp32 maximum pmf,
 // good to 2^-23, which settles most; what that leaves open needs the fp64 maximum, unless
@@ -541,7 +592,10 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NV <= 2 ? 4 : 3) : 1) sv_
                 for (int e = 0; e < VEC; ++e) y[e] *= inv;
                 if (wide)
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) y[e] = ms > 0.0 && i + e < g.d ? (float)(in64.prod(i + e) / sqrt(ms)) : 0.f;
+                    for (int e = 0; e < VEC; ++e) {
+                        const double p = i + e < g.d ? in64.prod(i + e) : 0.0;
+                        y[e] = p != 0.0 ? (float)(p / sqrt(ms)) : 0.f;
+                    }
                 if (AL) *reinterpret_cast<uint4*>(static_cast<char*>(g.normed) + (base + i) * ESZ) = q8_pack<ESZ>(y);
                 else outs[j * nthr + tid] = q8_pack<ESZ>(y);
             }
@@ -554,7 +608,10 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NV <= 2 ? 4 : 3) : 1) sv_
         // 8 * 2^-24 |t| of a half
         const bool near = !bad && (tiny || far > 0.5f - 0x1p-21f * tm * k);
         double dm = pmf;  // the maximum, as exactly as it is needed
-        if (__any_sync(0xffffffffu, near)) dm = q8_near<ESZ, NV, RES, AL>(g, in64.x, in64.residual, row, pmf, k, s_pm[set], near);
+        if (__any_sync(0xffffffffu, near)) {
+            if (pm == 0u && q8_zero_row<ESZ, NV, RES, AL>(g, in64.x, in64.residual, row)) dm = 0.0;
+            else dm = q8_near<ESZ, NV, RES, AL>(g, in64.x, in64.residual, row, pmf, k, s_pm[set], near);
+        }
         if (tid == 0) g.scale[row] = bad ? NAN : (dm > 0.0 ? (float)(dm / (127.0 * sqrt(ms))) : 0.f);
     }
 }
