@@ -578,8 +578,22 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NV <= 2 ? 4 : 3) : 1) sv_
         double ms = 1.0;  // by all where g.normed, else by the first thread
         if (g.norm && (tid == 0 || g.normed)) ms = (again ? sd : (double)ss) / g.d + (double)g.eps;
         if (g.normed) {
-            const bool wide = !bad && (tiny || ms < 0x1p-200 || ms > 0x1p200);  // 1 / rms, or p, leaves fp32
+            // 1 / rms, or p, leaves fp32; or a p of this thread is subnormal, and its quotient by a
+            // small rms would have no more bits than it has
+            bool wide = !bad && (tiny || ms < 0x1p-200 || ms > 0x1p200);
             const float inv = bad ? NAN : (ms > 0.0 ? (float)(1.0 / sqrt(ms)) : 0.f);
+            if (inv > 1.f) {
+                float least = FLT_MIN;
+#pragma unroll
+                for (int e = 0; e < NV * P; ++e) {
+                    const int i = (e / P * nthr + tid) * VEC + 2 * (e % P);
+                    float u, v;
+                    unpack2(p2[e], u, v);
+                    if (AL ? e / P < mine : i < g.d) least = fminf(least, fabsf(u));
+                    if (AL ? e / P < mine : i + 1 < g.d) least = fminf(least, fabsf(v));
+                }
+                wide |= least < FLT_MIN;
+            }
             if (!AL && g.sum) sync_row();  // the sums have left
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
