@@ -463,8 +463,9 @@ sv_status spec_verify_lowrank_head(const void* h, const void* w_down, const void
  * last hidden states are normed and quantised, a scale for each token, and
  * multiplied with weights quantised once, a scale for each channel.  Products and
  * sums are exact (int32); a logit's roundings are those of the sum to fp32, of the two
- * multiplications by its scales, and of its output type.  Infrastructure around [SlimSpec, Metodologia,
- * "Arquitetura": the draft's LM head W_full h]; the pages give no 8-bit form.
+ * multiplications by its scales, and of its output type.  Infrastructure around
+ * [SlimSpec, Metodologia, "Arquitetura": the draft's LM head W_full h]; the pages give
+ * no 8-bit form.
  *
  * An int8 matrix [rows][K] has a row pitch ld (bytes): a multiple of 16, at least K
  * ((K + 15) / 16 * 16 is the least).  The bytes of a row past K are neither read nor
@@ -559,18 +560,21 @@ size_t spec_verify_beam_workspace_size(int B, int W, int V, int K, sv_dtype dt);
  *   score        [B][W] float;  temperature [B] float
  *   frozen       optional [B][W] int32, nonzero = frozen; pad_token in [0, V) then
  *   out_parent   [B][K] int32: w;  out_token [B][K] int32: v;  out_score [B][K]
- *                float: the key (evaluated in fp64), the next level's score.  Slots
- *                past the candidates hold -1, -1 and -inf.
+ *                float: the key (evaluated in fp64), the next level's score; -inf
+ *                where it is below fp32's range, and no candidate there.  Slots past
+ *                the candidates hold -1, -1 and -inf.
  *   out_row_status  optional [B] int32: SV_ROW_BAD_TEMPERATURE (nothing but frozen
  *                beams is considered), SV_ROW_BAD_LOGITS (a row that is read holds NaN
  *                or +inf, is all -inf, or its logits / T leave fp32's range from
  *                above, or all of them from below; finite ones inside it are taken
- *                whatever their size, mask values like -1e30 among them), SV_ROW_BAD_SCORE (NaN or +inf); a
- *                beam at fault gives no candidate.
+ *                whatever their size, mask values like -1e30 among them),
+ *                SV_ROW_BAD_SCORE (NaN or +inf); a beam at fault gives no candidate.
  * Limits: W and K in [1, SV_MAX_BEAMS], V in [1, SV_BEAM_MAX_V].  Two launches.
  * spec_verify_tree's output law is the target's for children drawn independently
  * from q; the best children are not that (greedy trees, verified with T = 0,
- * excepted).  The key's fp32 sums decide between beams whose keys agree to ~1e-7.
+ * excepted).  A key is within 2^-19 of its value (2^-18 where logits / T pass 2^24),
+ * the rounding to float apart: candidates of different beams whose keys agree to
+ * twice that may come in either order.
  */
 sv_status spec_verify_beam_select(const void* logits, sv_dtype dt, const float* score, const float* temperature,
                                   const int32_t* frozen, int pad_token, int B, int W, int V, int K, int32_t* out_parent,

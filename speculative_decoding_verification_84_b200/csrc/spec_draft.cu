@@ -76,7 +76,7 @@ cudaError_t q8_rows_go(const Q8RowsArgs& g, int threads, cudaStream_t st)
 
 // A row by one warp, without barriers across warps, where 4 vectors a thread are enough,
 // else by up to 256 threads with as few vectors each as that allows, else by up to 1024;
-// rows that shared memory cannot hold three of, from memory, three times.
+// rows that shared memory cannot hold three of, from memory, twice.
 template <int ESZ, bool RES, bool AL>
 cudaError_t q8_rows_launch(const Q8RowsArgs& g, cudaStream_t st)
 {

@@ -18,9 +18,13 @@
 //                  by counting.  The sequence's first CTA (or the last to finish)
 //                  places the beams' candidates by their keys (fp64) the same way.
 //                  A programmatic dependent of sv_beam_rows.
-// Selecting inside the pass (each CTA its segment's K best, with group maxima for
-// a threshold) cost more than the pass: 64 x 8 x 128256 bf16, K = 8, took 49 us in
-// that form against 27 us for the pass and 12 for the pick.
+// Selecting inside the pass (each CTA its segment's K best, with group maxima for a
+// threshold) cost more than the pass does: 64 x 8 x 128256 bf16, K = 8, took 96 us in
+// that form and 46 when first parted; now 37.8, of which the pass is 27.
+// Rows of many equal logits (all of them, say) leave the counting for one look a pick:
+// 66 us of that shape flat, 329 with K = 32 (54 otherwise).  A row that counts for nothing
+// is not read, but its warps have nothing else to do: a first level of that shape, one
+// live beam of eight, takes 26 us.
 // Batches are cut by token index, so equal rows give equal normalisers wherever
 // they lie in memory.
 //
@@ -65,9 +69,9 @@ __device__ __forceinline__ bool beam_t_ok(float T) { return T == 0.f || (T >= SV
 
 // Integer offset of a batch's sum: of its maximum, kept finite where a batch holds only
 // the type's lowest values (its sum is then 0).  T = 0 (khi = 1) needs the NaN test only.
-// Up to kBeamOffset the offset is within 32 of the maximum's exponent (fp32 steps by 16 or
-// 32 there, and klo adds up to 16), so a batch's sum lies in fp32's range and keeps terms
-// down to 2^-94 of the largest.  Beyond it the sum may be anything, 0 or infinite
+// Up to kBeamOffset the offset is within 48 of the maximum's exponent (fp32 steps by up to
+// 32 there, and klo adds up to 32), so a batch's sum lies in fp32's range and keeps terms
+// down to 2^-78 of the largest.  Beyond it the sum may be anything, 0 or infinite
 // included: such a batch counts for nothing beside a maximum within the bound, and
 // where the row's own maximum is beyond it the normaliser is taken again in fp64.
 constexpr float kBeamOffset = 0x1p28f;

@@ -31,7 +31,8 @@ def _run(sa, sw, dtype, K=100, zeros=True):
         w[::5] = 0
     a, w = a.to(DEV)[:, :K], w.to(DEV)[:, :K]
     z = binding.q8_matmul(a, sa.to(DEV), w, sw.to(DEV), dtype)
-    want = ref.q8_matmul(a.cpu().numpy(), ref.f64(sa), w.cpu().numpy(), ref.f64(sw))
+    with np.errstate(invalid="ignore"):  # 0 times an infinite scale
+        want = ref.q8_matmul(a.cpu().numpy(), ref.f64(sa), w.cpu().numpy(), ref.f64(sw))
     return ref.f64(z), want
 
 
