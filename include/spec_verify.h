@@ -78,7 +78,11 @@ typedef enum { SV_DTYPE_F32 = 0, SV_DTYPE_BF16 = 1 } sv_dtype;
  * never trap; they are reported here).  With bit 1, 2, 4 or 16 the sequence
  * emits n_accepted = 0 and out_tokens all -1. */
 #define SV_ROW_BAD_TOKEN 1        /* some draft token outside [0, V) */
-#define SV_ROW_BAD_LOGITS 2       /* a row that is read holds NaN or +inf, or is all -inf */
+#define SV_ROW_BAD_LOGITS 2       /* a row that is read holds NaN or +inf, or is all -inf;
+                                     a row whose |logits| / T pass ~10^9 may be reported
+                                     too, a mask value like -1e10 over a long stretch among
+                                     them (spec_verify_beam_select takes those; -inf masks
+                                     are taken everywhere) */
 #define SV_ROW_BAD_TEMPERATURE 4  /* T < 0, NaN, +inf, or 0 < T < SV_TEMPERATURE_MIN */
 #define SV_ROW_RESIDUAL_ZERO 8    /* residual mass below 2^-18 (it counts as vanished);
                                      the token was drawn from p_n instead */

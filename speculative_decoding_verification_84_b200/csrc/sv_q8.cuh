@@ -11,7 +11,7 @@
 //   sv_q8_rows       CTAs walk rows, the next one on its way to shared memory
 //   sv_q8_rows_long  rows that shared memory cannot hold three of: read twice from
 //                    memory, fp64 throughout
-// Bound by bytes and instructions: 16384 x 4096 bf16 with a residual takes 95 us, 4.9
+// Bound by bytes and instructions: 16384 x 4096 bf16 with a residual takes 93 us, 5.0
 // TB/s of the 470 MB it cannot do without.
 //
 // The product.  z[m][v] = sa[m] sw[v] sum_k a[m][k] w[v][k] on the tensor cores
@@ -19,8 +19,8 @@
 // 128 * 128 * K both below 2^31).  The weights are the MMA's 128 rows and the
 // tokens its columns, so a small batch pads to 16 tokens, not to 128, and every
 // weight byte crosses to an SM once per token tile (up to 256 tokens; 320 in a tile of
-// two).  Bound by the weights' bytes up to some 250 tokens (1 x 4096 x 128256: 83 us, 6.3
-// TB/s), above by the tensor cores at the power limit (2048 x 4096 x 151936: 810 us, 3.1
+// two).  Bound by the weights' bytes up to some 250 tokens (1 x 4096 x 128256: 82 us, 6.4
+// TB/s), above by the tensor cores at the power limit (2048 x 4096 x 151936: 800 us, 3.2
 // P operations a second; at 32000 columns the tensor pipe is active for 81 %).
 //   warp 0     TMA: per stage two K blocks of 128 x 128 bytes of weights and nt x 128 of
 //              tokens, 128-byte swizzle, an mbarrier ring
